@@ -75,6 +75,7 @@ typedef enum {
 #define SCHNET_FLAG_NONFINITE 0x4u
 #define SCHNET_FLAG_BADTYPE   0x8u
 #define SCHNET_FLAG_TIMEOUT   0x10u
+#define SCHNET_FLAG_BADINDEX  0x20u   /* schnet_preference_loss: a pair names no replica */
 
 /* Filter-network weight storage (flag for channel-wise 16-bit weights,
  * FlashSchNet summary, How: "channel-wise 16-bit quantization").  Each
@@ -301,6 +302,133 @@ SCHNET_API schnet_status schnet_build_neighbors_noalloc(const float *d_pos, int3
                                                         int32_t periodic, const float *box, int32_t *d_row_ptr,
                                                         int32_t *d_col, int32_t *d_rev, int64_t edge_capacity,
                                                         int64_t *d_n_edges, uint32_t *d_flags, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * Readout tuning: the trunk's output features of many conformations kept in 8
+ * bits, readout energies and weight gradients from them, and a preference loss
+ * over pairs of conformations.  The pages have no counterpart (they use a trained
+ * model as it is); these calls let a user adapt the readout of a potential to
+ * conformations this library samples, and run on with it:
+ *   features x^L -> schnet_store_features / schnet_get_features (once a frame, the
+ *   trunk's weights being fixed) -> schnet_readout_energy -> schnet_preference_loss
+ *   -> schnet_readout_gradients -> the caller's optimizer -> schnet_set_readout.
+ * The calls without a context are enqueued on cuda_stream (a cudaStream_t, NULL =
+ * legacy default stream) of the current device, to which every device pointer
+ * belongs; they neither allocate nor synchronize and may be captured into a graph.
+ * Calls may overlap on the GPU when they share no buffer they write (workspaces
+ * included).  Results do not depend on scheduling: the same inputs give the same
+ * bits.  A CUDA error already pending on the calling thread is left in place and
+ * reported as SCHNET_ERR_CUDA before anything is enqueued. */
+
+/* Element types of schnet_store_features and schnet_preference_loss. */
+typedef enum {
+    SCHNET_FLOAT32 = 0,
+    SCHNET_FLOAT16 = 1,
+    SCHNET_BFLOAT16 = 2,
+    SCHNET_FLOAT64 = 3
+} schnet_float_dtype;
+
+/* Features in 8 bits, one scale a row.  With a_i = max_f |x_if|, row i's scale is
+ * 2^e, e the smallest integer >= -100 with a_i <= 448 * 2^e, and code_if is x_if / 2^e
+ * rounded to the nearest e4m3 value (ties to even); the stored value 2^e code_if
+ * is within 2^-4 |x_if| (or 2^(e-10), where that is more) of x_if.  The division is
+ * exact, so nothing but this rounding is lost.  A row with a NaN, an infinity or a
+ * magnitude of 2^127 or more gets a NaN scale: all that is formed from it is NaN.
+ *   d_x: device [n_atoms] rows of n_features elements of type dtype (FLOAT32,
+ *     FLOAT16, BFLOAT16), row_stride elements (>= n_features) apart
+ *   d_codes: device uint8 [n_atoms][W], W = n_features rounded up to a multiple
+ *     of 16 (columns past n_features are set to 0), 16-byte aligned
+ *   d_scales: device uint8 [n_atoms]: e + 127; 255 = NaN
+ * n_features even, 2..128; n_atoms >= 0.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+SCHNET_API schnet_status schnet_store_features(const void *d_x, int32_t dtype, int64_t n_atoms, int32_t n_features,
+                                               int64_t row_stride, uint8_t *d_codes, uint8_t *d_scales,
+                                               void *cuda_stream);
+
+/* The features x^L of the context's last evaluation (schnet_energy_forces or the
+ * last step of schnet_step), stored as by schnet_store_features in the caller's atom
+ * order: d_codes [N][W], d_scales [N].  On the context's stream.
+ * Errors: INVALID_ARG, STATE (no evaluation since the list was built), CUDA. */
+SCHNET_API schnet_status schnet_get_features(schnet_ctx *ctx, uint8_t *d_codes, uint8_t *d_scales);
+
+/* Replace the context's readout by host float32 weights, shaped as in
+ * schnet_weights (R1 [F][F/2], c1, R2 [F/2]): packs them as schnet_create does and
+ * blocks until they are on the device.  The next evaluation and schnet_step use
+ * them; a following schnet_step with resume = 1 re-evaluates the forces first.
+ * Errors: INVALID_ARG, CUDA. */
+SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, const float *h_c1, const float *h_R2,
+                                            float c2);
+
+/* Readout weights on the device: R1 [F][F/2], c1, R2 [F/2], c2 [1], float32. */
+typedef struct {
+    const float *R1, *c1, *R2, *c2;
+} schnet_readout;
+
+/* Readout energies from stored features: eps_i = ssp(x_i R1 + c1) R2 + c2 with x_i
+ * the stored value, E_r = sum of eps_i over o_r <= i < o_{r+1} (formed in float64,
+ * rounded once; 0 for an empty replica).
+ *   d_codes [n_atoms][W], d_scales [n_atoms] as stored above
+ *   d_replica_offsets: device int32 [n_replicas+1], 0 <= o_0 <= ... <= o_R <= n_atoms
+ *     (values outside [0, n_atoms] are read as the nearer end)
+ *   d_energy: device float32 [n_replicas]; d_eps: device float32 [n_atoms]; entries
+ *     of atoms in no replica are written too
+ *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
+ * Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
+SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
+                                               int32_t n_features, int32_t n_replicas,
+                                               const int32_t *d_replica_offsets, const schnet_readout *w,
+                                               float *d_energy, float *d_eps, void *d_workspace, size_t ws_bytes,
+                                               void *cuda_stream);
+
+/* Gradients of sum_r g_r E_r (g_r = d_grad_energy[r], e.g. dL/dE_r of a loss L) with
+ * respect to the readout's weights, from stored features (the hidden layer is
+ * formed again, nothing of the forward pass is read):
+ *   dp_ih = g_r(i) R2_h sigma(p_ih); dR1 = x^T dp; dc1 = sum_i dp_i;
+ *   dR2 = sum_i g_r(i) ssp(p_i); dc2 = sum_i g_r(i)
+ * Atoms in no replica, or in one with g_r = 0, add nothing, even with a NaN scale.
+ *   d_dR1 [F][F/2], d_dc1, d_dR2 [F/2], d_dc2 [1]: device float32, overwritten
+ * Arguments and errors otherwise as schnet_readout_energy. */
+SCHNET_API schnet_status schnet_readout_gradients(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
+                                                  int32_t n_features, int32_t n_replicas,
+                                                  const int32_t *d_replica_offsets, const schnet_readout *w,
+                                                  const float *d_grad_energy, float *d_dR1, float *d_dc1,
+                                                  float *d_dR2, float *d_dc2, void *d_workspace, size_t ws_bytes,
+                                                  void *cuda_stream);
+
+/* Device workspace bytes of schnet_readout_energy and schnet_readout_gradients on
+ * the current device.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+SCHNET_API schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t n_features, size_t *bytes);
+
+/* Preference loss over pairs of conformations (w preferred to l, e.g. native and
+ * decoy), forward and backward.  Under p(x) ~ exp(-E(x)/kT) the partition function
+ * cancels in a pair's log ratio against a reference potential,
+ *   m_p = -[(E_w - Eref_w) - (E_l - Eref_l)] / kT      (no reference: Eref = 0),
+ *   L = mean over pairs of (1 - s) ln(1 + e^-m_p) + s ln(1 + e^m_p),   s = smoothing,
+ *   c_p = sigma(m_p) - (1 - s);  dL/dE_w -= c_p / (kT P), dL/dE_l += c_p / (kT P),
+ * P the number of pairs that count.  A pair with an index of -1 is padding: margin 0,
+ * no part in L or P.  So is a pair with any other index outside [0, n_replicas),
+ * which raises SCHNET_FLAG_BADINDEX; a NaN margin raises SCHNET_FLAG_NONFINITE and
+ * makes the loss and its two gradients NaN.
+ *   d_energy, d_reference: device [n_replicas] of type dtype (FLOAT32 or FLOAT64);
+ *     d_reference may be NULL
+ *   d_pairs: device int32 [n_pairs][2] = (w, l), 8-byte aligned; w = l is allowed
+ *   d_loss: device float64 [1] (0 without pairs); d_margins: device float32
+ *     [n_pairs] or NULL; d_grad_energy: device float32 [n_replicas], overwritten
+ *   d_flags: device uint32 [1] or NULL: receives the bits of this call
+ * Margins and the loss are float64 inside.  The pairs' slopes are summed per replica
+ * as 64-bit integers, which add up to the same value in any order; with b the bits of
+ * n_pairs, a slope is kept to 2^-25 of itself down to 2^(2b - 76) and to 2^(2b - 101)
+ * below that.
+ * kT > 0; 0 <= smoothing <= 1; 1 <= n_replicas; 0 <= n_pairs < 2^31.
+ * Errors: INVALID_ARG, CUDA. */
+SCHNET_API schnet_status schnet_preference_loss(const void *d_energy, const void *d_reference, int32_t dtype,
+                                                int32_t n_replicas, const int32_t *d_pairs, int64_t n_pairs,
+                                                double kT, double smoothing, double *d_loss, float *d_margins,
+                                                float *d_grad_energy, uint32_t *d_flags, void *d_workspace,
+                                                size_t ws_bytes, void *cuda_stream);
+
+/* Device workspace bytes of schnet_preference_loss (256-byte aligned base).
+ * Errors: INVALID_ARG. */
+SCHNET_API schnet_status schnet_preference_workspace_bytes(int32_t n_replicas, int64_t n_pairs, size_t *bytes);
 
 /* Number of device kernels the library has launched on this context so far
  * (graph replays count each kernel node). */

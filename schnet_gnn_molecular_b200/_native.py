@@ -15,12 +15,15 @@ OK = 0
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "CUDA", 3: "CAPACITY", 4: "SKIN", 5: "NONFINITE", 6: "BADTYPE",
                 7: "STATE", 8: "TIMEOUT", 9: "UNSUPPORTED"}
 FLAG_CAPACITY, FLAG_SKIN, FLAG_NONFINITE, FLAG_BADTYPE, FLAG_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+FLAG_BADINDEX = 0x20
 WEIGHT_DTYPES = {"fp32": 0, "fp16": 1, "bf16": 2, "fp16fast": 3}
 
 EXPORTED = ["schnet_workspace_bytes", "schnet_create", "schnet_build_neighbors", "schnet_energy_forces",
             "schnet_step", "schnet_step_host", "schnet_get_status", "schnet_last_error", "schnet_destroy",
             "schnet_get_neighbors", "schnet_get_atom_energies", "schnet_kernel_launches", "schnet_profile_steps",
-            "schnet_build_neighbors_noalloc", "schnet_test_exp2", "schnet_test_timeout"]
+            "schnet_build_neighbors_noalloc", "schnet_test_exp2", "schnet_test_timeout", "schnet_store_features",
+            "schnet_get_features", "schnet_set_readout", "schnet_readout_energy", "schnet_readout_gradients",
+            "schnet_readout_workspace_bytes", "schnet_preference_loss", "schnet_preference_workspace_bytes"]
 KERNEL_CLASSES = ["cfconv_fwd", "cfconv_bwd", "atomwise", "neighbors", "forces", "integrate", "reduce", "mask",
                   "cfconv_dh"]
 
@@ -46,6 +49,10 @@ class StepParams(C.Structure):
     _fields_ = [("dt_fs", C.c_float), ("gamma_per_ps", C.c_float), ("temperature_K", C.c_float),
                 ("n_rebuild", C.c_int32), ("seed", C.c_uint64), ("step0", C.c_uint64),
                 ("d_noise", C.c_void_p), ("resume", C.c_int32), ("use_graph", C.c_int32)]
+
+
+class Readout(C.Structure):
+    _fields_ = [(k, C.c_void_p) for k in ("R1", "c1", "R2", "c2")]
 
 
 _lib = None
@@ -79,6 +86,16 @@ def load() -> C.CDLL:
     L.schnet_profile_steps.argtypes = [vp, vp, vp, vp, vp, C.c_int64, C.POINTER(StepParams), dp, i64p]
     L.schnet_build_neighbors_noalloc.argtypes = [vp, C.c_int32, C.c_int32, vp, C.c_float, C.c_float, C.c_int32,
                                                  C.POINTER(C.c_float), vp, vp, vp, C.c_int64, vp, vp, vp]
+    i32, i64, sz, szp = C.c_int32, C.c_int64, C.c_size_t, C.POINTER(C.c_size_t)
+    L.schnet_store_features.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp]
+    L.schnet_get_features.argtypes = [vp, vp, vp]
+    L.schnet_set_readout.argtypes = [vp, vp, vp, vp, C.c_float]
+    L.schnet_readout_energy.argtypes = [vp, vp, i32, i32, i32, vp, C.POINTER(Readout), vp, vp, vp, sz, vp]
+    L.schnet_readout_gradients.argtypes = [vp, vp, i32, i32, i32, vp, C.POINTER(Readout), vp, vp, vp, vp, vp, vp, sz,
+                                           vp]
+    L.schnet_readout_workspace_bytes.argtypes = [i32, i32, szp]
+    L.schnet_preference_loss.argtypes = [vp, vp, i32, i32, vp, i64, C.c_double, C.c_double, vp, vp, vp, vp, vp, sz, vp]
+    L.schnet_preference_workspace_bytes.argtypes = [i32, i64, szp]
     L.schnet_kernel_launches.argtypes = [vp]
     L.schnet_kernel_launches.restype = C.c_int64
     for name in EXPORTED:

@@ -153,6 +153,28 @@ class SchNet:
         self._check(self.lib.schnet_get_atom_energies(self.ctx, _ptr(out)), "get_atom_energies")
         return out
 
+    def features(self):
+        """(codes, scales): the trunk's output features of the last evaluation in 8 bits, as store_features
+        gives them, in the caller's atom order."""
+        W = feature_width(self.cfg.n_features)
+        codes = torch.empty((self.n_atoms, W), dtype=torch.float8_e4m3fn, device=self.device)
+        scales = torch.empty(self.n_atoms, dtype=torch.float8_e8m0fnu, device=self.device)
+        self._check(self.lib.schnet_get_features(self.ctx, _ptr(codes), _ptr(scales)), "features")
+        return codes, scales
+
+    def set_readout(self, readout):
+        """Replace the readout by {"R1", "c1", "R2", "c2"} (tensors or arrays, shaped as in the weights)."""
+        F = self.cfg.n_features
+        host = {}
+        for k, n in (("R1", F * (F // 2)), ("c1", F // 2), ("R2", F // 2), ("c2", 1)):
+            v = readout[k].detach().cpu().numpy() if isinstance(readout[k], torch.Tensor) else readout[k]
+            host[k] = np.ascontiguousarray(np.asarray(v, dtype=np.float32))
+            if host[k].size != n or (k == "R1" and host[k].shape != (F, F // 2)):
+                raise ValueError(f"set_readout: {k} has shape {host[k].shape}")
+        vp = lambda a: C.c_void_p(a.ctypes.data)
+        self._check(self.lib.schnet_set_readout(self.ctx, vp(host["R1"]), vp(host["c1"]), vp(host["R2"]),
+                                                float(host["c2"].reshape(-1)[0])), "set_readout")
+
     def profile_steps(self, pos, vel, types, mass, n_steps, *, dt=4.0, gamma=0.1, temperature=300.0, n_rebuild=20,
                       seed=0, step0=0, resume=True):
         """Eager steps with CUDA events around every kernel on the library stream.
@@ -168,6 +190,132 @@ class SchNet:
 
     def kernel_launches(self) -> int:
         return int(self.lib.schnet_kernel_launches(self.ctx))
+
+
+# ----------------------------------------------------------------------
+# readout tuning: tensors in, tensors out, on the current stream of their device
+# ----------------------------------------------------------------------
+def feature_width(F: int) -> int:
+    """Columns of a row of stored features: F rounded up to a multiple of 16."""
+    return (F + 15) // 16 * 16
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) with the tensors' device current and its current stream."""
+    with torch.cuda.device(device):
+        st = fn(*args, C.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+    if st != nat.OK:
+        raise SchNetError(st, fn.__name__)
+
+
+def _scratch(device, size_fn, *args):
+    """A workspace of the bytes that size_fn names, from the caching allocator (so calls on different
+    streams, or captured into different graphs, never share one)."""
+    n = C.c_size_t(0)
+    with torch.cuda.device(device):
+        st = size_fn(*args, C.byref(n))
+    if st != nat.OK:
+        raise SchNetError(st, size_fn.__name__)
+    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+
+def store_features(x: torch.Tensor):
+    """(codes, scales) of the rows of x [n, F] (float32, float16 or bfloat16; unit column stride): e4m3 codes
+    [n, feature_width(F)] (zeros past F) and one power-of-two scale a row [n]; the stored value is
+    codes.float()[:, :F] * scales.float()[:, None].  See schnet_store_features in include/schnet.h."""
+    _require(x.is_cuda and x.dim() == 2, "store_features: x must be a 2-d CUDA tensor")
+    _require(x.dtype in _STORE_DTYPES, f"store_features: dtype {x.dtype}")
+    n, F = x.shape
+    _require(n == 0 or (x.stride(1) == 1 and (n == 1 or x.stride(0) >= F)),
+             "store_features: columns must be adjacent and rows must not overlap")
+    codes = torch.empty((n, feature_width(F)), dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(n, dtype=torch.float8_e8m0fnu, device=x.device)
+    _call(x.device, nat.load().schnet_store_features, _ptr(x), _STORE_DTYPES[x.dtype], n, F, max(x.stride(0), F),
+          _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def _readout_args(codes, scales, replica_offsets, readout):
+    dev = codes.device
+    R1, c1, R2, c2 = (readout[k] for k in ("R1", "c1", "R2", "c2"))
+    for k, t in (("codes", codes), ("scales", scales), ("replica_offsets", replica_offsets), ("R1", R1), ("c1", c1),
+                 ("R2", R2), ("c2", c2)):
+        _require(t.is_cuda and t.device == dev and t.is_contiguous(), f"{k} must be a contiguous tensor on {dev}")
+    for k, t in (("R1", R1), ("c1", c1), ("R2", R2), ("c2", c2)):
+        _require(t.dtype == torch.float32, f"{k} must be float32")
+    _require(R1.dim() == 2 and R1.shape[0] == 2 * R1.shape[1], f"R1 must be [F, F / 2], is {tuple(R1.shape)}")
+    F, H = R1.shape
+    _require(c1.shape == (H,) and R2.shape == (H,) and c2.numel() == 1, "c1, R2 must be [F / 2] and c2 one value")
+    _require(codes.dim() == 2 and codes.shape[1] == feature_width(F) and codes.element_size() == 1,
+             f"codes must be [n, {feature_width(F)}] bytes")
+    n = codes.shape[0]
+    _require(scales.shape == (n,) and scales.element_size() == 1, "scales must be [n] bytes")
+    _require(replica_offsets.dim() == 1 and replica_offsets.numel() >= 2 and replica_offsets.dtype == torch.int32,
+             "replica_offsets must be int32 [R + 1]")
+    _require(n < 2 ** 31, "too many atoms")
+    w = nat.Readout(R1.data_ptr(), c1.data_ptr(), R2.data_ptr(), c2.data_ptr())
+    ws = _scratch(dev, nat.load().schnet_readout_workspace_bytes, n, F)
+    R = replica_offsets.numel() - 1
+    return dev, F, H, R, ws, (_ptr(codes), _ptr(scales), n, F, R, _ptr(replica_offsets), C.byref(w))
+
+
+def readout_energy(codes, scales, replica_offsets, readout):
+    """(energy [R], eps [n]) float32: readout energies from stored features.  replica_offsets int32 [R + 1] on the
+    device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
+    dev, _, _, R, ws, args = _readout_args(codes, scales, replica_offsets, readout)
+    energy = torch.empty(R, dtype=torch.float32, device=dev)
+    eps = torch.empty(codes.shape[0], dtype=torch.float32, device=dev)
+    _call(dev, nat.load().schnet_readout_energy, *args, _ptr(energy), _ptr(eps), _ptr(ws), ws.numel())
+    return energy, eps
+
+
+def readout_gradients(codes, scales, replica_offsets, readout, grad_energy):
+    """{"R1", "c1", "R2", "c2"}: gradients of sum_r grad_energy[r] E_r with respect to the readout's weights, from
+    stored features; grad_energy float32 [R] (e.g. the third result of preference_loss)."""
+    dev, F, H, R, ws, args = _readout_args(codes, scales, replica_offsets, readout)
+    _require(grad_energy.device == dev and grad_energy.dtype == torch.float32 and grad_energy.shape == (R,)
+             and grad_energy.is_contiguous(), f"grad_energy must be contiguous float32 [{R}] on {dev}")
+    out = {k: torch.empty(s, dtype=torch.float32, device=dev) for k, s in
+           (("R1", (F, H)), ("c1", (H,)), ("R2", (H,)), ("c2", (1,)))}
+    _call(dev, nat.load().schnet_readout_gradients, *args, _ptr(grad_energy), *(_ptr(out[k]) for k in out), _ptr(ws),
+          ws.numel())
+    return out
+
+
+def preference_loss(energy, pairs, *, kT, reference=None, smoothing=0.0, flags=None):
+    """(loss [] float64, margins [P] float32, grad_energy [R] float32) of the preference loss over pairs [P, 2]
+    (preferred, rejected) of conformations, int32 on the device; -1 marks padding.  energy and reference: float32 or
+    float64 [R]; kT in the energies' unit; flags: optional int32 [1] tensor that receives the SCHNET_FLAG_* bits of
+    this call.  See schnet_preference_loss in include/schnet.h."""
+    dev = energy.device
+    _require(energy.is_cuda and energy.dim() == 1 and energy.numel() >= 1 and energy.is_contiguous()
+             and energy.dtype in _ENERGY_DTYPES, "energy must be a contiguous float32 or float64 CUDA tensor [R]")
+    if reference is not None:
+        _require(reference.device == dev and reference.dtype == energy.dtype and reference.shape == energy.shape
+                 and reference.is_contiguous(), "reference must be like energy")
+    _require(pairs.device == dev and pairs.dtype == torch.int32 and pairs.dim() == 2 and pairs.shape[1] == 2
+             and pairs.is_contiguous(), "pairs must be contiguous int32 [P, 2] on the energies' device")
+    _require(flags is None or (flags.device == dev and flags.numel() == 1 and flags.element_size() == 4),
+             "flags must be one 32-bit integer on the energies' device")
+    R, P = energy.numel(), pairs.shape[0]
+    lib = nat.load()
+    ws = _scratch(dev, lib.schnet_preference_workspace_bytes, R, P)
+    loss = torch.empty((), dtype=torch.float64, device=dev)
+    margins = torch.empty(P, dtype=torch.float32, device=dev)
+    grad = torch.empty(R, dtype=torch.float32, device=dev)
+    _call(dev, lib.schnet_preference_loss, _ptr(energy), _ptr(reference), _ENERGY_DTYPES[energy.dtype], R,
+          _ptr(pairs), P, float(kT), float(smoothing), _ptr(loss), _ptr(margins), _ptr(grad), _ptr(flags), _ptr(ws),
+          ws.numel())
+    return loss, margins, grad
+
+
+_STORE_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_ENERGY_DTYPES = {torch.float32: 0, torch.float64: 3}
 
 
 def from_workload(w, weights: dict, device=None, edge_capacity=0, weight_dtype=None) -> SchNet:

@@ -261,6 +261,20 @@ void pad_mat(const float* src, int rin, int cin, float* dst, int rout, int cout_
         }
 }
 
+// The readout's two tensor-core images (R1^T forward, R1 backward, adjacent) with their
+// scales, and its padded vectors.
+void pack_readout(const float* R1, const float* c1, const float* R2, float c2, int F, int Hh, uint8_t* img, float* sc,
+                  float* pc1, float* pR2, float* pc2)
+{
+    pack_aw(R1, F, Hh, true, img, sc);
+    pack_aw(R1, F, Hh, false, img + AW_IMG, sc + FP);
+    for (int k = 0; k < HP; ++k) {
+        pc1[k] = k < Hh ? c1[k] : 0.f;
+        pR2[k] = k < Hh ? R2[k] : 0.f;
+    }
+    pc2[0] = c2;
+}
+
 void build_weight_blob(const schnet_ctx* c, const schnet_weights* wt, uint8_t* wsbase, uint8_t* blob,
                        size_t wbegin)
 {
@@ -303,8 +317,8 @@ void build_weight_blob(const schnet_ctx* c, const schnet_weights* wt, uint8_t* w
         for (int j = 0; j < 6; ++j)
             pack_aw(mats[j], F, F, j < 3, H(w.aw_img) + (size_t)(6 * l + j) * AW_IMG, H(w.aw_sc) + (size_t)(6 * l + j) * FP);
     }
-    pack_aw(wt->R1, F, Hh, true, H(w.aw_img) + (size_t)(6 * L) * AW_IMG, H(w.aw_sc) + (size_t)(6 * L) * FP);
-    pack_aw(wt->R1, F, Hh, false, H(w.aw_img) + (size_t)(6 * L + 1) * AW_IMG, H(w.aw_sc) + (size_t)(6 * L + 1) * FP);
+    pack_readout(wt->R1, wt->c1, wt->R2, wt->c2, F, Hh, H(w.aw_img) + (size_t)(6 * L) * AW_IMG,
+                 H(w.aw_sc) + (size_t)(6 * L) * FP, H(w.c1), H(w.R2), H(w.c2));
     pad_mat(wt->emb, c->T, F, H(w.emb), c->T, FP, false);
     // x0 = emb[z] has one row per type, so h0 = x0 W_in of interaction 0 does too (float64 sums)
     for (int t = 0; t < c->T; ++t)
@@ -314,11 +328,6 @@ void build_weight_blob(const schnet_ctx* c, const schnet_weights* wt, uint8_t* w
                 for (int k = 0; k < F; ++k) acc += (double)wt->emb[(size_t)t * F + k] * (double)wt->W_in[(size_t)k * F + f];
             H(w.emb_h0)[(size_t)t * FP + f] = (float)acc;
         }
-    for (int k = 0; k < HP; ++k) {
-        H(w.c1)[k] = k < Hh ? wt->c1[k] : 0.f;
-        H(w.R2)[k] = k < Hh ? wt->R2[k] : 0.f;
-    }
-    H(w.c2)[0] = wt->c2;
     // replica tables
     for (int r = 0; r <= c->R; ++r) H(w.rep_off)[r] = c->rep_off[r];
     int32_t* ar = H(w.atom_rep);
@@ -481,6 +490,7 @@ schnet_status step_impl(schnet_ctx* c, float* pos, float* vel, const int32_t* ty
     double* ek = ekin ? ekin : c->ws.ekin;
     if (!p->resume || !c->forces_valid) {
         c->have_list = false;            // fresh start: the build below replaces the list
+        c->have_features = false;
         CK(launch_build_neighbors(c, pos));
         c->have_list = true;
         CK(launch_energy_forces(c, types, ep, nullptr, true));
@@ -508,6 +518,7 @@ schnet_status step_impl(schnet_ctx* c, float* pos, float* vel, const int32_t* ty
         }
     }
     c->forces_valid = true;
+    c->have_features = true;
     return SCHNET_OK;
 }
 
@@ -647,6 +658,7 @@ schnet_status schnet_build_neighbors(schnet_ctx* c, const float* d_pos)
     if (!c || !d_pos) return SCHNET_ERR_INVALID_ARG;
     join_in(c);
     c->have_list = false;
+    c->have_features = false;
     CK(launch_build_neighbors(c, d_pos));
     c->have_list = true;
     c->forces_valid = false;
@@ -663,6 +675,7 @@ schnet_status schnet_energy_forces(schnet_ctx* c, const float* d_pos, const int3
     CK(launch_pack_positions(c, d_pos));
     CK(launch_energy_forces(c, d_types, d_energy, d_forces, d_forces != nullptr));
     c->forces_valid = false;
+    c->have_features = true;
     CK(join_out(c));
     return SCHNET_OK;
 }
@@ -757,6 +770,36 @@ schnet_status schnet_get_atom_energies(schnet_ctx* c, float* d_eps)
     join_in(c);
     CK(launch_scatter_atoms(c, c->ws.eps, d_eps));
     CK(join_out(c));
+    return SCHNET_OK;
+}
+
+schnet_status schnet_get_features(schnet_ctx* c, uint8_t* d_codes, uint8_t* d_scales)
+{
+    if (!c || !d_codes || !d_scales || ((uintptr_t)d_codes & 15)) return SCHNET_ERR_INVALID_ARG;
+    if (!c->have_features) return fail(c, SCHNET_ERR_STATE, "schnet_get_features: no evaluation since the list was built");
+    join_in(c);
+    CK(launch_get_features(c, d_codes, d_scales));
+    CK(join_out(c));
+    return SCHNET_OK;
+}
+
+schnet_status schnet_set_readout(schnet_ctx* c, const float* h_R1, const float* h_c1, const float* h_R2, float c2)
+{
+    if (!c || !h_R1 || !h_c1 || !h_R2) return SCHNET_ERR_INVALID_ARG;
+    Workspace& w = c->ws;
+    std::vector<uint8_t> img(2 * AW_IMG, 0);
+    std::vector<float> sc(2 * FP), v1(HP), v2(HP);
+    float v3 = 0.f;
+    pack_readout(h_R1, h_c1, h_R2, c2, c->F, c->H, img.data(), sc.data(), v1.data(), v2.data(), &v3);
+    join_in(c);
+    const size_t id = 6 * (size_t)c->L;
+    CK(cudaMemcpyAsync(w.aw_img + id * AW_IMG, img.data(), img.size(), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.aw_sc + id * FP, sc.data(), sc.size() * sizeof(float), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.c1, v1.data(), HP * sizeof(float), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.R2, v2.data(), HP * sizeof(float), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.c2, &v3, sizeof(float), cudaMemcpyHostToDevice, c->s));
+    c->forces_valid = false;      // the stored forces are the old readout's
+    CK(cudaStreamSynchronize(c->s));
     return SCHNET_OK;
 }
 

@@ -164,6 +164,7 @@ struct schnet_ctx {
     schnet::Workspace ws;
     bool have_list = false;
     bool forces_valid = false;
+    bool have_features = false;     // ws.x holds the trunk's output of an evaluation over the current list
     // MD phase: steps taken since the last neighbour build
     int since_build = 0;
     // graph cache: 0 = build + n_rebuild steps, 1 = build + one step, 2 = one step
@@ -198,6 +199,7 @@ cudaError_t launch_b_kick(schnet_ctx* c, float* d_vel, const float* d_mass, floa
 cudaError_t launch_set_step(schnet_ctx* c, unsigned long long step);
 cudaError_t launch_forces(schnet_ctx* c, float* d_forces);
 cudaError_t launch_replica_sum(schnet_ctx* c, const float* v, double* out);
+cudaError_t launch_get_features(schnet_ctx* c, uint8_t* d_codes, uint8_t* d_scales);
 cudaError_t launch_embed(schnet_ctx* c, const int32_t* types);
 cudaError_t launch_aw_fwd(schnet_ctx* c, int layer);
 cudaError_t launch_aw_bwd_top(schnet_ctx* c);

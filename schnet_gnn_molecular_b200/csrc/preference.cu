@@ -1,0 +1,247 @@
+// Preference loss over pairs of conformations: forward and gradient in one pass
+// over the pairs (no counterpart on the pages).
+//
+// Under p(x) ~ exp(-E(x)/kT), ln p_w - ln p_l = -(E_w - E_l)/kT: the partition
+// function cancels.  m = -[(E_w - Eref_w) - (E_l - Eref_l)]/kT; a pair's loss is
+// (1-s) ln(1+e^-m) + s ln(1+e^m), its slope c = dL/dm = sigma(m) - (1-s), |c| <= 1.
+// The gradient scatters -c to w and +c to l.  A replica may be in any number of pairs,
+// so the scatter is an atomic sum; it is made of 64-bit integers, whose sum does not
+// depend on the order, so the gradient is the same bits every run:
+//   word 0: c in units of 2^-s0, s0 = 62 - b, b = bits of n_pairs (|sum| < 2^62);
+//   word 1: the slopes below 2^(24-s0), which word 0 would keep to less than 2^-25
+//           of themselves, in units of 2^-s1, s1 = 2 s0 - 24 (|sum| < 2^62 again).
+// A pair's slope goes to one of the two words, so there are two atomics a pair.
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+
+namespace schnet {
+
+constexpr int PT = 256;                  // threads per CTA
+constexpr int PREF_MAX_CTA = 148 * 8;
+
+struct PrefPartial {
+    double loss;
+    long long count;
+    unsigned int flags, pad;
+};
+
+struct PrefArgs {
+    const void *energy, *reference;
+    const int2* pairs;
+    long long P;
+    int R;
+    double inv_kT, s;
+    int s0, s1;
+    double* loss;
+    float *margins, *grad;
+    uint32_t* flags;
+    unsigned long long *w0, *w1;         // [R] slope sums, zeroed before the pair pass
+    unsigned char* bad;                  // [R] 1: a NaN margin touches the replica
+    PrefPartial* partial;                // [CTAs of the pair pass]
+};
+
+// a pair's margin; false where the pair does not count
+template <class T>
+__device__ __forceinline__ bool pair_margin(const PrefArgs& a, int2 q, double& m, unsigned int& flags)
+{
+    m = 0.0;
+    if ((unsigned)q.x >= (unsigned)a.R || (unsigned)q.y >= (unsigned)a.R) {
+        if (q.x < -1 || q.x >= a.R || q.y < -1 || q.y >= a.R) flags |= SCHNET_FLAG_BADINDEX;
+        return false;
+    }
+    const T* E = static_cast<const T*>(a.energy);
+    const T* B = static_cast<const T*>(a.reference);
+    double dw = (double)__ldg(E + q.x), dl = (double)__ldg(E + q.y);
+    if (B) {
+        dw -= (double)__ldg(B + q.x);
+        dl -= (double)__ldg(B + q.y);
+    }
+    m = -(dw - dl) * a.inv_kT;
+    return true;
+}
+
+// loss and slope of a margin: t = e^-|m|, ln(1+e^-|m|) = log1p(t), and the logistic of
+// the sign that does not cancel
+__device__ __forceinline__ void pair_loss(double m, double s, double& loss, double& c)
+{
+    const double t = exp(-fabs(m));
+    const double r = 1.0 / (1.0 + t);
+    loss = log1p(t);
+    if (m < 0.0 && s < 1.0) loss -= (1.0 - s) * m;
+    if (m > 0.0 && s > 0.0) loss += s * m;         // (an infinite margin times a weight of 0 is 0)
+    if (isnan(m)) loss = m;
+    const double sneg = m >= 0.0 ? t * r : r;      // sigma(-m)
+    c = s - sneg;                                  // = sigma(m) - (1 - s), no cancellation at s = 0
+}
+
+template <class T>
+__global__ void __launch_bounds__(PT) k_pref_pairs(PrefArgs a)
+{
+    double loss = 0.0;
+    long long count = 0;
+    unsigned int flags = 0;
+    const double u0 = __longlong_as_double((long long)(1023 + a.s0) << 52);
+    const double u1 = __longlong_as_double((long long)(1023 + a.s1) << 52);
+    const double small = __longlong_as_double((long long)(1023 + 24 - a.s0) << 52);
+    for (long long p = (long long)blockIdx.x * PT + threadIdx.x; p < a.P; p += (long long)gridDim.x * PT) {
+        const int2 q = __ldg(a.pairs + p);
+        double m, l, c;
+        const bool ok = pair_margin<T>(a, q, m, flags);
+        if (a.margins) a.margins[p] = (float)m;
+        if (!ok) continue;
+        pair_loss(m, a.s, l, c);
+        loss += l;
+        count += 1;
+        if (isnan(m)) {
+            flags |= SCHNET_FLAG_NONFINITE;
+            a.bad[q.x] = 1;
+            a.bad[q.y] = 1;
+            continue;
+        }
+        const bool fine = fabs(c) < small;
+        const long long v = __double2ll_rn(c * (fine ? u1 : u0));
+        unsigned long long* w = fine ? a.w1 : a.w0;
+        if (v != 0 && q.x != q.y) {
+            atomicAdd(w + q.x, (unsigned long long)(-v));
+            atomicAdd(w + q.y, (unsigned long long)v);
+        }
+    }
+    // the CTA's sums in a fixed order
+    __shared__ double sl[PT / 32];
+    __shared__ long long sc[PT / 32];
+    __shared__ unsigned int sf[PT / 32];
+    for (int o = 16; o > 0; o >>= 1) {
+        loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if ((threadIdx.x & 31) == 0) {
+        sl[threadIdx.x >> 5] = loss;
+        sc[threadIdx.x >> 5] = count;
+        sf[threadIdx.x >> 5] = flags;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        PrefPartial t{0.0, 0, 0u, 0u};
+        for (int w = 0; w < PT / 32; ++w) {
+            t.loss += sl[w];
+            t.count += sc[w];
+            t.flags |= sf[w];
+        }
+        a.partial[blockIdx.x] = t;
+    }
+}
+
+__global__ void __launch_bounds__(PT) k_pref_finish(PrefArgs a, int nparts)
+{
+    __shared__ double sl[PT];
+    __shared__ long long sc[PT];
+    __shared__ unsigned int sf;
+    if (threadIdx.x == 0) sf = 0;
+    __syncthreads();
+    double loss = 0.0;
+    long long count = 0;
+    unsigned int flags = 0;
+    for (int k = threadIdx.x; k < nparts; k += PT) {
+        const PrefPartial t = a.partial[k];
+        loss += t.loss;
+        count += t.count;
+        flags |= t.flags;
+    }
+    sl[threadIdx.x] = loss;
+    sc[threadIdx.x] = count;
+    if (flags) atomicOr(&sf, flags);
+    __syncthreads();
+    for (int o = PT / 2; o > 0; o >>= 1) {
+        if (threadIdx.x < o) {
+            sl[threadIdx.x] += sl[threadIdx.x + o];
+            sc[threadIdx.x] += sc[threadIdx.x + o];
+        }
+        __syncthreads();
+    }
+    const double inv = sc[0] > 0 ? 1.0 / (double)sc[0] : 0.0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.loss = sl[0] * inv;
+        if (a.flags) *a.flags = sf;
+    }
+    const double k0 = a.inv_kT * inv * __longlong_as_double((long long)(1023 - a.s0) << 52);
+    const double k1 = a.inv_kT * inv * __longlong_as_double((long long)(1023 - a.s1) << 52);
+    for (int r = blockIdx.x * PT + threadIdx.x; r < a.R; r += gridDim.x * PT) {
+        float g = (float)((double)(long long)a.w0[r] * k0 + (double)(long long)a.w1[r] * k1);
+        if (a.bad[r]) g = __int_as_float(0x7fffffff);
+        a.grad[r] = g;
+    }
+}
+
+static size_t pref_carve(int R, uint8_t* base, PrefArgs& a)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    size_t off = 0;
+    a.w0 = reinterpret_cast<unsigned long long*>(base + off);
+    off += up((size_t)R * 8);
+    a.w1 = reinterpret_cast<unsigned long long*>(base + off);
+    off += up((size_t)R * 8);
+    a.bad = base + off;
+    off += up((size_t)R);
+    a.partial = reinterpret_cast<PrefPartial*>(base + off);
+    off += up(sizeof(PrefPartial) * PREF_MAX_CTA);
+    return off;
+}
+
+}  // namespace schnet
+
+using namespace schnet;
+
+extern "C" schnet_status schnet_preference_workspace_bytes(int32_t n_replicas, int64_t n_pairs, size_t* bytes)
+{
+    if (!bytes || n_replicas < 1 || n_pairs < 0 || n_pairs > 0x7fffffffLL) return SCHNET_ERR_INVALID_ARG;
+    PrefArgs a{};
+    *bytes = pref_carve(n_replicas, nullptr, a);
+    return SCHNET_OK;
+}
+
+extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void* d_reference, int32_t dtype,
+                                                int32_t n_replicas, const int32_t* d_pairs, int64_t n_pairs,
+                                                double kT, double smoothing, double* d_loss, float* d_margins,
+                                                float* d_grad_energy, uint32_t* d_flags, void* d_workspace,
+                                                size_t ws_bytes, void* cuda_stream)
+{
+    size_t need = 0;
+    if (!d_energy || !d_loss || !d_grad_energy || !d_workspace || ((uintptr_t)d_workspace & 255) ||
+        (dtype != SCHNET_FLOAT32 && dtype != SCHNET_FLOAT64) || !(kT > 0.0) || !std::isfinite(kT) ||
+        !(smoothing >= 0.0 && smoothing <= 1.0) ||
+        schnet_preference_workspace_bytes(n_replicas, n_pairs, &need) != SCHNET_OK || ws_bytes < need ||
+        (n_pairs > 0 && !d_pairs) || ((uintptr_t)d_pairs & 7))
+        return SCHNET_ERR_INVALID_ARG;
+    if (cudaPeekAtLastError() != cudaSuccess) return SCHNET_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    PrefArgs a{};
+    pref_carve(n_replicas, (uint8_t*)d_workspace, a);
+    a.energy = d_energy;
+    a.reference = d_reference;
+    a.pairs = reinterpret_cast<const int2*>(d_pairs);
+    a.P = n_pairs;
+    a.R = n_replicas;
+    a.inv_kT = 1.0 / kT;
+    a.s = smoothing;
+    int b = 0;
+    while ((n_pairs >> b) > 0) ++b;
+    a.s0 = 62 - b;
+    a.s1 = 2 * a.s0 - 24;
+    a.loss = d_loss;
+    a.margins = d_margins;
+    a.grad = d_grad_energy;
+    a.flags = d_flags;
+    const int g1 = (int)std::max<int64_t>(1, std::min<int64_t>((n_pairs + PT - 1) / PT, PREF_MAX_CTA));
+    const int g2 = std::min((n_replicas + PT - 1) / PT, PREF_MAX_CTA);
+    if (cudaMemsetAsync(d_workspace, 0, (uint8_t*)a.partial - (uint8_t*)d_workspace, s) != cudaSuccess)
+        return SCHNET_ERR_CUDA;
+    if (dtype == SCHNET_FLOAT64)
+        k_pref_pairs<double><<<g1, PT, 0, s>>>(a);
+    else
+        k_pref_pairs<float><<<g1, PT, 0, s>>>(a);
+    k_pref_finish<<<g2, PT, 0, s>>>(a, g1);
+    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+}

@@ -1,0 +1,83 @@
+"""Refused calls of the readout-tuning entry points: argument errors come back before any CUDA call, so they
+are checked without a GPU."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from schnet_gnn_molecular_b200 import _native as nat
+from schnet_gnn_molecular_b200 import api, build
+
+P = C.c_void_p(4096)          # a pointer that no refused call follows
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return nat.load()
+
+
+def test_store_refusals(lib):
+    ok = dict(x=P, dtype=0, n=4, F=64, stride=64, codes=P, scales=P)
+    def call(**kw):
+        a = {**ok, **kw}
+        return lib.schnet_store_features(a["x"], a["dtype"], a["n"], a["F"], a["stride"], a["codes"], a["scales"], None)
+    assert call(F=0) == 9 and call(F=3) == 9 and call(F=130) == 9
+    for bad in (dict(x=None), dict(codes=None), dict(scales=None), dict(dtype=3), dict(dtype=-1), dict(n=-1),
+                dict(stride=63), dict(codes=C.c_void_p(4104)), dict(x=C.c_void_p(4098))):
+        assert call(**bad) == 1, bad
+
+
+def test_readout_refusals(lib):
+    w = nat.Readout(4096, 4096, 4096, 4096)
+    no = nat.Readout(4096, None, 4096, 4096)
+    big = 1 << 40
+    def energy(codes=P, scales=P, n=8, F=64, R=2, off=P, w=w, e=P, eps=P, ws=P, size=big):
+        return lib.schnet_readout_energy(codes, scales, n, F, R, off, C.byref(w) if w else None, e, eps, ws, size, None)
+    def grad(codes=P, scales=P, n=8, F=64, R=2, off=P, w=w, g=P, d=P, ws=P, size=big):
+        return lib.schnet_readout_gradients(codes, scales, n, F, R, off, C.byref(w) if w else None, g, P, P, P, d, ws,
+                                            size, None)
+    for f in (energy, grad):
+        assert f(F=3) == 9 and f(F=0) == 9 and f(F=256) == 9
+        for bad in (dict(codes=None), dict(scales=None), dict(n=-1), dict(R=0), dict(off=None), dict(w=None),
+                    dict(w=no), dict(ws=None), dict(ws=C.c_void_p(4100)), dict(size=64), dict(codes=C.c_void_p(4097))):
+            assert f(**bad) == 1, (f, bad)
+    assert energy(e=None) == 1 and energy(eps=None) == 1 and grad(g=None) == 1 and grad(d=None) == 1
+    n = C.c_size_t(0)
+    assert lib.schnet_readout_workspace_bytes(100, 64, C.byref(n)) == 0 and n.value > 0
+    assert lib.schnet_readout_workspace_bytes(100, 63, C.byref(n)) == 9
+    assert lib.schnet_readout_workspace_bytes(-1, 64, C.byref(n)) == 1
+    assert lib.schnet_readout_workspace_bytes(1, 64, None) == 1
+
+
+def test_preference_refusals(lib):
+    need = C.c_size_t(0)
+    assert lib.schnet_preference_workspace_bytes(16, 9, C.byref(need)) == 0
+    def call(e=P, ref=None, dtype=0, R=16, pairs=P, n=9, kT=0.6, s=0.0, loss=P, m=None, g=P, ws=P, size=need.value):
+        return lib.schnet_preference_loss(e, ref, dtype, R, pairs, n, kT, s, loss, m, g, None, ws, size, None)
+    for bad in (dict(e=None), dict(dtype=1), dict(dtype=2), dict(R=0), dict(pairs=None), dict(n=-1), dict(n=2 ** 31),
+                dict(kT=0.0), dict(kT=-1.0), dict(kT=float("nan")), dict(kT=float("inf")), dict(s=-0.1), dict(s=1.1),
+                dict(s=float("nan")), dict(loss=None), dict(g=None), dict(ws=None), dict(ws=C.c_void_p(4100)),
+                dict(size=need.value - 1), dict(pairs=C.c_void_p(4100))):
+        assert call(**bad) == 1, bad
+    assert lib.schnet_preference_workspace_bytes(0, 1, C.byref(need)) == 1
+    assert lib.schnet_preference_workspace_bytes(1, 1, None) == 1
+
+
+def test_context_calls_refuse_null(lib):
+    assert lib.schnet_get_features(None, P, P) == 1
+    assert lib.schnet_set_readout(None, P, P, P, 0.0) == 1
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        api.store_features(x)
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    w = {"R1": torch.zeros(64, 32), "c1": torch.zeros(32), "R2": torch.zeros(32), "c2": torch.zeros(1)}
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        api.readout_energy(codes, scales, off, w)
+    with pytest.raises(ValueError):
+        api.preference_loss(torch.zeros(4), torch.zeros(1, 2, dtype=torch.int32), kT=1.0)
