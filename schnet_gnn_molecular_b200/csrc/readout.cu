@@ -7,6 +7,7 @@
 // x alone, whatever computes them.
 #include <algorithm>
 
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -112,8 +113,9 @@ cudaError_t launch_get_features(schnet_ctx* c, uint8_t* codes, uint8_t* scales)
 // ---------------------------------------------------------------------------
 // readout energies
 // ---------------------------------------------------------------------------
-constexpr int RT = 256;                  // threads per CTA
-constexpr int RTILE = 32;                // atoms a CTA stages at a time
+constexpr int RT = 256;                  // threads per CTA of the gradient kernels
+constexpr int RTILE = 32;                // atoms a CTA of theirs stages at a time
+constexpr int MAX_SM = 256;              // status words: one per CTA
 
 struct ReadoutArgs {
     const uint8_t *codes, *scales;
@@ -121,6 +123,9 @@ struct ReadoutArgs {
     const int32_t* off;
     const float *R1, *c1, *R2, *c2;
     float *energy, *eps;
+    double* csum;                        // [ceil(n / 32)] sums of 32 atoms' eps
+    uint32_t* status;                    // [CTAs] 1: a device-side wait gave up
+    int ncta;
     const float* gE;
     float *dR1, *dc1, *dR2, *dc2;
     float* part;                         // [CTAs][F H + 2 H] partial gradients
@@ -128,6 +133,288 @@ struct ReadoutArgs {
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
+
+// x^L tiles come by TMA: 128 rows of 128 bytes, 128-byte swizzled (16-byte piece c of
+// row r lies at piece c ^ (r & 7)), so that a warp whose lanes each read their own row
+// meets every bank once per 8 lanes.  Columns past W and rows past n read as zero.
+constexpr uint32_t TILE_BYTES = 128 * 128;
+constexpr uint32_t RO_POLLS = 1u << 22;
+
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int row, uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(TILE_BYTES)
+                 : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// two e4m3 codes -> fp16 pair (exact)
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// barrier of nthreads threads; true when every one of them passed true
+__device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ok), "r"(id), "r"(nthreads)
+                 : "memory");
+    return r != 0;
+}
+
+// R1 as the MMA's B operand [64 h][128 f] (K-major core matrices), two fp16 terms of
+// R1 2^s with 2^s the power of two that brings the largest |R1| to [2^14, 2^15): hi + lo
+// carry 22 bits, and entries 2^-24 of the largest still lose nothing above 2^-39 of it.
+// Returns 2^-s.  All threads of the CTA; red: one float per warp.
+constexpr uint32_t R1_TERM = HP * FP * 2;
+__device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, float* red)
+{
+    float mx = 0.f;
+    const int total = a.F * a.H;
+    for (int k = threadIdx.x; k < total; k += blockDim.x) mx = fmaxf(mx, fabsf(__ldg(a.R1 + k)));
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    mx = 0.f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) mx = fmaxf(mx, red[w]);
+    const int ex = (int)(__float_as_uint(mx) >> 23);
+    int s = ex > 0 && ex < 255 ? 14 - (ex - 127) : 0;
+    s = max(-110, min(110, s));
+    const float up = __uint_as_float((uint32_t)(127 + s) << 23);
+    for (int k = threadIdx.x; k < HP * FP / 2; k += blockDim.x) {
+        const int h = k % HP, f = k / HP * 2;                   // two inputs of one hidden unit
+        const float v0 = h < a.H && f < a.F ? __ldg(a.R1 + f * a.H + h) * up : 0.f;
+        const float v1 = h < a.H && f + 1 < a.F ? __ldg(a.R1 + (f + 1) * a.H + h) * up : 0.f;
+        uint32_t vh, vl;
+        split2<0>(v0, v1, vh, vl);
+        *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
+        *reinterpret_cast<uint32_t*>(lo + kmajor_off(h, f, HP)) = vl;
+    }
+    return __uint_as_float((uint32_t)(127 - s) << 23);
+}
+
+// the factor that takes an accumulator of row i (codes times R1 2^s) to p log2(e)
+__device__ __forceinline__ float row_factor(int byte, float down)
+{
+    if (byte == 255) return __int_as_float(0x7fffffff);
+    return fminf(__uint_as_float((uint32_t)byte << 23) * down, 1e38f) * LOG2EF;
+}
+
+// Energies.  Four groups of 4 warps share the CTA's R1; each takes every (4 gridDim)-th
+// tile of 128 atoms, one atom per thread: its row of codes is read from the TMA stage,
+// widened to fp16 (exact) and put into tensor memory as the MMA's A operand (lane = atom),
+// so D[atom][h] = codes . R1 comes back with a whole hidden layer per thread and the sum
+// over h needs no exchange.  The next tile's MMAs run under this tile's epilogue.
+// Bound: the 2 transcendentals per hidden unit (MUFU: 8 cycles an atom and SM) and HBM
+// (133 bytes: 5.9 cycles); three quarters of the exponentials go to the FMA pipe.
+constexpr int FWD_GROUPS = 4, FWD_STAGES = 2, FWD_THREADS = FWD_GROUPS * 128;
+constexpr uint32_t FWD_STAGE0 = 0;
+constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
+constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
+constexpr uint32_t FWD_RED = FWD_CST + 32 * 16;
+constexpr uint32_t FWD_BAR = FWD_RED + 64;
+constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * (FWD_STAGES + 1) + 16 + 1024;
+
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    float4* cst = reinterpret_cast<float4*>(sm + FWD_CST);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + FWD_BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + FWD_GROUPS * (FWD_STAGES + 1));
+    const int warp = threadIdx.x >> 5, g = threadIdx.x >> 7, t = threadIdx.x & 127;
+    uint64_t* full = bars + g * (FWD_STAGES + 1);
+    uint64_t* done = full + FWD_STAGES;
+
+    pdl_trigger();
+    if (warp == 0) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < FWD_GROUPS * (FWD_STAGES + 1); ++k) mbar_init(bars + k, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 32) {
+        const int h = threadIdx.x * 2;
+        const bool i0 = h < a.H, i1 = h + 1 < a.H;
+        cst[threadIdx.x] = make_float4(i0 ? __ldg(a.c1 + h) * LOG2EF : 0.f, i1 ? __ldg(a.c1 + h + 1) * LOG2EF : 0.f,
+                                       i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
+    }
+    const float down = stage_r1(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<float*>(sm + FWD_RED));
+    const float c2 = __ldg(a.c2);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem = *tslot + 128 * g;                       // A: 64 columns, D: 64 columns
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t stage0 = smem_u32(sm) + FWD_STAGE0 + g * FWD_STAGES * TILE_BYTES;
+    const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x, gid = blockIdx.x + gridDim.x * g;
+    const int nt = gid < ntiles ? (ntiles - gid + ngroups - 1) / ngroups : 0;
+    auto row0 = [&](int it) { return (gid + it * ngroups) * 128; };
+    auto scale_of = [&](int it) { return it < nt && row0(it) + t < a.n ? (int)__ldg(a.scales + row0(it) + t) : 127; };
+    const uint32_t id = idesc_f16(128, HP, 0, 0);
+    const uint64_t bhi = smem_desc(smem_u32(sm) + FWD_R1, HP * 16, 128);
+    const uint64_t blo = smem_desc(smem_u32(sm) + FWD_R1 + R1_TERM, HP * 16, 128);
+    bool ok = true;
+
+    // codes of tile it -> tensor memory
+    auto widen = [&](int it) {
+        const int st = it % FWD_STAGES;
+        ok &= mbar_wait_bounded(full + st, (uint32_t)(it / FWD_STAGES) & 1u, RO_POLLS);
+        __syncwarp();
+        const uint32_t row = stage0 + st * TILE_BYTES + t * 128;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 q = lds128(row + (((half * 4 + c) ^ (t & 7)) << 4));
+                codes_to_half(q.x, v[c * 8 + 0], v[c * 8 + 1]);
+                codes_to_half(q.y, v[c * 8 + 2], v[c * 8 + 3]);
+                codes_to_half(q.z, v[c * 8 + 4], v[c * 8 + 5]);
+                codes_to_half(q.w, v[c * 8 + 6], v[c * 8 + 7]);
+            }
+            tmem_st32(tmem + lanes + half * 32, v);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    };
+    // all of the group's rows are in tensor memory: MMAs of tile it, and the stage's next tile
+    auto start = [&](int it) {
+        tc_fence_before();
+        ok = group_and(1 + g, 128, ok);
+        if (!ok) return;
+        if (t == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < FP / 16; ++ks)                  // the small terms first
+                mma_f16_ts(tmem + 64, tmem + ks * 8, blo + (uint64_t)((ks * 2 * HP * 16) >> 4), id, ks > 0 ? 1u : 0u);
+#pragma unroll
+            for (int ks = 0; ks < FP / 16; ++ks)
+                mma_f16_ts(tmem + 64, tmem + ks * 8, bhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id, 1u);
+            mma_commit(done);
+            if (it + FWD_STAGES < nt)
+                tma_tile(stage0 + (it % FWD_STAGES) * TILE_BYTES, &map, row0(it + FWD_STAGES), full + it % FWD_STAGES);
+        }
+        __syncwarp();
+    };
+
+    if (nt > 0) {
+        if (t == 0)
+            for (int it = 0; it < FWD_STAGES && it < nt; ++it)
+                tma_tile(stage0 + it * TILE_BYTES, &map, row0(it), full + it);
+        int byte = scale_of(0);
+        widen(0);
+        start(0);
+        for (int it = 0; it < nt && ok; ++it) {
+            const float k = row_factor(byte, down);
+            byte = scale_of(it + 1);
+            ok = mbar_wait_bounded(done, (uint32_t)it & 1u, RO_POLLS);
+            __syncwarp();
+            tc_fence_after();
+            float d[64];
+            tmem_ld32(tmem + lanes + 64, *reinterpret_cast<float(*)[32]>(d));
+            tmem_ld32(tmem + lanes + 96, *reinterpret_cast<float(*)[32]>(d + 32));
+            tmem_ld_wait();
+            if (it + 1 < nt) {
+                widen(it + 1);
+                start(it + 1);
+            }
+            float2 e0 = make_float2(0.f, 0.f), e1 = e0;
+            const float2 kk = dup2(k);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float4 c = cst[j];
+                const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
+                const float2 m = make_float2(-fabsf(p.x), -fabsf(p.y));
+                const float2 u = j % 4 != 3 ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
+                const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
+                e0 = fma2(make_float2(c.z, c.w), make_float2(lg2_mufu(y.x), lg2_mufu(y.y)), e0);
+                e1 = fma2(make_float2(c.z, c.w), make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)), e1);
+            }
+            const int i = row0(it) + t;
+            const float e = ((e0.x + e0.y) + (e1.x + e1.y)) + c2;
+            if (i < a.n) a.eps[i] = e;
+            double s = i < a.n ? (double)e : 0.0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if ((t & 31) == 0 && i < a.n) a.csum[i >> 5] = s;
+        }
+        // a wait gave up: let this group's copies and MMAs in flight end (bounded) before the memory goes
+        if (!ok && t == 0) {
+            for (int st = 0; st < FWD_STAGES; ++st)
+                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(full + st, ph, 1u << 12);
+            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done, ph, 1u << 12);
+        }
+    }
+    const int gave_up = __syncthreads_or(!ok);
+    if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up ? 1u : 0u;
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(*tslot, 512);
+    }
+}
+
+// E_r: TPR threads (a warp, or the CTA where replicas are long) add the sums of the 32-atom
+// chunks inside the replica and the single atoms at its ends, in float64 and a fixed order.
+template <int TPR>
+__global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
+{
+    pdl_wait();
+    uint32_t bad = 0;
+    for (int k = threadIdx.x; k < a.ncta; k += 256) bad |= a.status[k];
+    bad = __syncthreads_or((int)bad);
+    const int r = TPR == 256 ? (int)blockIdx.x : (int)(blockIdx.x * (256 / TPR) + threadIdx.x / TPR);
+    const int l = threadIdx.x % TPR;
+    double s = 0.0;
+    if (r < a.R) {
+        const int lo = off_at(a, r), hi = off_at(a, r + 1);
+        const int c0 = (lo + 31) >> 5, c1 = hi >> 5;             // whole chunks [c0, c1)
+        if (c0 < c1) {
+            for (int i = lo + l; i < c0 * 32; i += TPR) s += (double)a.eps[i];
+            for (int c = c0 + l; c < c1; c += TPR) s += a.csum[c];
+            for (int i = c1 * 32 + l; i < hi; i += TPR) s += (double)a.eps[i];
+        } else {
+            for (int i = lo + l; i < hi; i += TPR) s += (double)a.eps[i];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (TPR == 256) {
+        __shared__ double ws[8];
+        if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.0;
+        for (int w = 0; w < 8; ++w) s += ws[w];
+    }
+    if (l == 0 && r < a.R) a.energy[r] = bad ? __int_as_float(0x7fffffff) : (float)s;
+}
 
 // the replica of atom i, -1 for none: the last r with o_r <= i, if i < o_{r+1}
 __device__ __forceinline__ int replica_of(const ReadoutArgs& a, int i)
@@ -153,48 +440,6 @@ __device__ __forceinline__ void stage_features(const ReadoutArgs& a, int i0, flo
             v = b == 255 ? __int_as_float(0x7fffffff) : __half2float(__half(h)) * __uint_as_float((uint32_t)b << 23);
         }
         xs[k] = v;
-    }
-}
-
-__global__ void __launch_bounds__(RT) k_readout_eps(ReadoutArgs a)
-{
-    extern __shared__ float rsm[];
-    float* xs = rsm;                     // [RTILE][F]
-    float* w = rsm + RTILE * a.F;        // [F][H]
-    for (int k = threadIdx.x; k < a.F * a.H; k += RT) w[k] = a.R1[k];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float c2 = a.c2[0];
-    for (int i0 = blockIdx.x * RTILE; i0 < a.n; i0 += gridDim.x * RTILE) {
-        __syncthreads();
-        stage_features(a, i0, xs);
-        __syncthreads();
-        for (int k = warp; k < RTILE && i0 + k < a.n; k += RT / 32) {
-            float e = 0.f;
-            for (int h = lane; h < a.H; h += 32) {
-                float p = a.c1[h];
-                for (int f = 0; f < a.F; ++f) p = fmaf(xs[k * a.F + f], w[f * a.H + h], p);
-                e = fmaf(ssp(p), a.R2[h], e);
-            }
-            for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-            if (lane == 0) a.eps[i0 + k] = e + c2;
-        }
-    }
-}
-
-__global__ void __launch_bounds__(RT) k_readout_sums(ReadoutArgs a)
-{
-    const int r = blockIdx.x;
-    double s = 0.0;
-    const int hi = off_at(a, r + 1);
-    for (int i = off_at(a, r) + threadIdx.x; i < hi; i += RT) s += (double)a.eps[i];
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __shared__ double ws[RT / 32];
-    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int w = 0; w < RT / 32; ++w) t += ws[w];
-        a.energy[r] = (float)t;
     }
 }
 
@@ -283,6 +528,35 @@ __global__ void __launch_bounds__(RT) k_readout_grad_sum(ReadoutArgs a, int npar
     }
 }
 
+// SMs of the current device
+static int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 1;
+    return std::min(n, MAX_SM);
+}
+
+// tensor map of the codes: rows of W bytes, boxes of 128 rows x 128 bytes, 128-byte swizzle
+static bool code_map(const ReadoutArgs& a, CUtensorMap* map)
+{
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static Encode encode = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool got = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                         q == cudaDriverEntryPointSuccess;
+        return got ? reinterpret_cast<Encode>(p) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)a.W, (cuuint64_t)a.n}, stride[1] = {(cuuint64_t)a.W};
+    const cuuint32_t box[2] = {128, 128}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dim, stride, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static schnet_status readout_args(const uint8_t* codes, const uint8_t* scales, int32_t n, int32_t F, int32_t R,
                                   const int32_t* off, const schnet_readout* w, void* ws, size_t ws_bytes,
                                   ReadoutArgs& a)
@@ -328,7 +602,8 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
     if (!bytes || n_atoms < 0) return SCHNET_ERR_INVALID_ARG;
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
     const size_t H = n_features / 2;
-    *bytes = GRAD_CTA * (sizeof(double) + sizeof(float) * (n_features * H + 2 * H)) + 512;
+    *bytes = std::max(GRAD_CTA * (sizeof(double) + sizeof(float) * (n_features * H + 2 * H)) + 512,
+                      sizeof(uint32_t) * MAX_SM + sizeof(double) * (((size_t)n_atoms + 31) / 32));
     return SCHNET_OK;
 }
 
@@ -347,11 +622,21 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
     a.energy = d_energy;
     a.eps = d_eps;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    const size_t smem = sizeof(float) * (RTILE * a.F + a.F * a.H);
-    if (cudaFuncSetAttribute(k_readout_eps, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SCHNET_ERR_CUDA;
-    if (a.n > 0) k_readout_eps<<<std::min((a.n + RTILE - 1) / RTILE, 148 * 4), RT, smem, s>>>(a);
-    k_readout_sums<<<a.R, RT, 0, s>>>(a);
+    const int ntiles = (a.n + 127) / 128;
+    a.ncta = std::min(ntiles, sm_count());
+    a.status = (uint32_t*)d_workspace;
+    a.csum = (double*)(a.status + MAX_SM);
+    if (a.n > 0) {
+        CUtensorMap map;
+        if (!code_map(a, &map) || cudaFuncSetAttribute(k_readout_eps, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)FWD_SMEM) != cudaSuccess)
+            return SCHNET_ERR_CUDA;
+        k_readout_eps<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
+    }
+    // a warp per replica up to 4096 atoms a replica on average, else a CTA
+    cudaError_t e = (int64_t)a.n > (int64_t)a.R * 4096 ? launch_pdl(k_readout_sums<256>, a.R, 256, 0, s, a)
+                                                      : launch_pdl(k_readout_sums<32>, (a.R + 7) / 8, 256, 0, s, a);
+    if (e != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
 }
 
