@@ -113,8 +113,6 @@ cudaError_t launch_get_features(schnet_ctx* c, uint8_t* codes, uint8_t* scales)
 // ---------------------------------------------------------------------------
 // readout energies
 // ---------------------------------------------------------------------------
-constexpr int RT = 256;                  // threads per CTA of the gradient kernels
-constexpr int RTILE = 32;                // atoms a CTA of theirs stages at a time
 constexpr int MAX_SM = 256;              // status words: one per CTA
 
 struct ReadoutArgs {
@@ -128,8 +126,10 @@ struct ReadoutArgs {
     int ncta;
     const float* gE;
     float *dR1, *dc1, *dR2, *dc2;
-    float* part;                         // [CTAs][F H + 2 H] partial gradients
-    double* part2;                       // [CTAs] partial dc2
+    int ngroups;                         // groups of the gradient kernel that have tiles
+    float* part;                         // [ngroups][64 h][128 f] their sums of D2
+    double* part2;                       // [CTAs] shares of dc2
+    double* colpart;                     // [ngroups][4 warps][128] column sums of g sigma, g ssp / ln2
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
@@ -188,19 +188,21 @@ __device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
 // R1 as the MMA's B operand [64 h][128 f] (K-major core matrices), two fp16 terms of
 // R1 2^s with 2^s the power of two that brings the largest |R1| to [2^14, 2^15): hi + lo
 // carry 22 bits, and entries 2^-24 of the largest still lose nothing above 2^-39 of it.
-// Returns 2^-s.  All threads of the CTA; red: one float per warp.
+// Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the epilogues' exponentials
+// do not all keep a NaN).  All threads of the CTA; red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
-__device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, float* red)
+__device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, uint32_t* red)
 {
-    float mx = 0.f;
+    uint32_t mx = 0;                     // as bits, which order like the magnitudes
     const int total = a.F * a.H;
-    for (int k = threadIdx.x; k < total; k += blockDim.x) mx = fmaxf(mx, fabsf(__ldg(a.R1 + k)));
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int k = threadIdx.x; k < total; k += blockDim.x) mx = max(mx, __float_as_uint(__ldg(a.R1 + k)) & 0x7fffffffu);
+    if (threadIdx.x < a.H && (__float_as_uint(__ldg(a.c1 + threadIdx.x)) & 0x7fffffffu) >= 0x7f800000u) mx = 0x7f800000u;
+    mx = __reduce_max_sync(0xffffffffu, mx);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
     __syncthreads();
-    mx = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) mx = fmaxf(mx, red[w]);
-    const int ex = (int)(__float_as_uint(mx) >> 23);
+    mx = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) mx = max(mx, red[w]);
+    const int ex = (int)(mx >> 23);
     int s = ex > 0 && ex < 255 ? 14 - (ex - 127) : 0;
     s = max(-110, min(110, s));
     const float up = __uint_as_float((uint32_t)(127 + s) << 23);
@@ -213,13 +215,13 @@ __device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uin
         *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
         *reinterpret_cast<uint32_t*>(lo + kmajor_off(h, f, HP)) = vl;
     }
-    return __uint_as_float((uint32_t)(127 - s) << 23);
+    return ex == 255 ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 - s) << 23);
 }
 
 // the factor that takes an accumulator of row i (codes times R1 2^s) to p log2(e)
 __device__ __forceinline__ float row_factor(int byte, float down)
 {
-    if (byte == 255) return __int_as_float(0x7fffffff);
+    if (byte == 255 || down != down) return __int_as_float(0x7fffffff);
     return fminf(__uint_as_float((uint32_t)byte << 23) * down, 1e38f) * LOG2EF;
 }
 
@@ -265,7 +267,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         cst[threadIdx.x] = make_float4(i0 ? __ldg(a.c1 + h) * LOG2EF : 0.f, i1 ? __ldg(a.c1 + h + 1) * LOG2EF : 0.f,
                                        i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
     }
-    const float down = stage_r1(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<float*>(sm + FWD_RED));
+    const float down = stage_r1(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
     const float c2 = __ldg(a.c2);
     fence_proxy_async_smem();
     tc_fence_before();
@@ -416,115 +418,395 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
     if (l == 0 && r < a.R) a.energy[r] = bad ? __int_as_float(0x7fffffff) : (float)s;
 }
 
-// the replica of atom i, -1 for none: the last r with o_r <= i, if i < o_{r+1}
-__device__ __forceinline__ int replica_of(const ReadoutArgs& a, int i)
+// ---------------------------------------------------------------------------
+// readout weight gradients
+// ---------------------------------------------------------------------------
+// Two groups of 8 warps share the CTA's R1; each takes a run of consecutive tiles.  A
+// thread holds one atom and half of its hidden units.  Per tile:
+//   GEMM1  D1[atom][h] = codes . R1 as in the energies;
+//   epilogue  per (atom, h): sigma(p), ssp(p); the column sums of g sigma and g ssp stay
+//     in registers, and sigma g_i scale_i goes to shared memory as an fp16 hi + residual pair;
+//   GEMM2  D2[f][h] += codes^T (sigma g scale): both operands are read MN-major, so the
+//     tile of codes widened once serves as it lies, and D2 stays in tensor memory from tile
+//     to tile.  R2 is a factor of whole columns and is applied at the very end.
+// The pair's power-of-two scale 2^E brings the largest |g_i scale_i| seen so far to
+// [2^13, 2^14); when a tile has a larger one, D2 is emptied first and E lowered.  The
+// tensor core's fp32 accumulation does not round to nearest, so D2 is emptied into fp32
+// sums in global memory every GRAD_FLUSH tiles in any case, and the column sums are folded
+// into float64 every GRAD_FOLD tiles.
+constexpr int GRAD_GROUPS = 2, GRAD_STAGES = 2, GRAD_THREADS = GRAD_GROUPS * 256;
+constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
+constexpr uint32_t GRAD_X = GRAD_STAGES * TILE_BYTES;            // within a group: codes as fp16 [128][128]
+constexpr uint32_t GRAD_B = GRAD_X + 128 * 128 * 2;              // [128][64 hi | 64 residual]
+constexpr uint32_t GRAD_GROUP = GRAD_B + 128 * 128 * 2;
+constexpr uint32_t GRAD_R1 = GRAD_GROUPS * GRAD_GROUP;
+constexpr uint32_t GRAD_CST = GRAD_R1 + 2 * R1_TERM;             // float[64]: c1 log2e
+constexpr uint32_t GRAD_RED = GRAD_CST + 64 * 4;
+constexpr uint32_t GRAD_ROW = GRAD_RED + 64;                     // per group: float2[128] (g, factor)
+constexpr uint32_t GRAD_MAX = GRAD_ROW + GRAD_GROUPS * 128 * 8;  // per group: uint32[4]
+constexpr uint32_t GRAD_SUM = GRAD_MAX + GRAD_GROUPS * 16;       // double[16]: the warps' parts of dc2
+constexpr uint32_t GRAD_BAR = GRAD_SUM + 16 * 8;
+constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * GRAD_GROUPS * (GRAD_STAGES + 2) + 16;
+static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
+constexpr int PART = HP * FP;                                    // one group's D2 sums, [h][f]
+
+// sums of v[0..31] over the warp's lanes: lane c gets column c's
+__device__ __forceinline__ float fold_columns(float (&v)[32])
 {
-    if (i < off_at(a, 0) || i >= off_at(a, a.R)) return -1;
-    int lo = 0, hi = a.R - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (off_at(a, mid) <= i) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int k = 0; k < s; ++k) {
+            const float keep = up ? v[k + s] : v[k], send = up ? v[k] : v[k + s];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float rcp_mufu(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D[tmem] (+)= A[smem desc] B[smem desc], kind::f16
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// last r >= from with o_r <= i (o_from <= i), by doubling steps and bisection
+__device__ __forceinline__ int advance_replica(const ReadoutArgs& a, int from, int i)
+{
+    int lo = from, step = 1;
+    while (lo + step < a.R && off_at(a, lo + step) <= i) {
+        lo += step;
+        step *= 2;
+    }
+    int hi = min(lo + step, a.R);                                // o_hi > i, or hi = R
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off_at(a, mid) <= i) lo = mid; else hi = mid;
     }
     return lo;
 }
 
-// stage x_i (stored values) of the tile's atoms as [RTILE][F]
-__device__ __forceinline__ void stage_features(const ReadoutArgs& a, int i0, float* xs)
+__global__ void __launch_bounds__(GRAD_THREADS, 1)
+k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 {
-    for (int k = threadIdx.x; k < RTILE * a.F; k += RT) {
-        const int i = i0 + k / a.F, f = k % a.F;
-        float v = 0.f;
-        if (i < a.n) {
-            const int b = a.scales[i];
-            const __half_raw h = __nv_cvt_fp8_to_halfraw(a.codes[(size_t)i * a.W + f], __NV_E4M3);
-            v = b == 255 ? __int_as_float(0x7fffffff) : __half2float(__half(h)) * __uint_as_float((uint32_t)b << 23);
-        }
-        xs[k] = v;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + GRAD_BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + GRAD_GROUPS * (GRAD_STAGES + 2));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = threadIdx.x >> 8, t = threadIdx.x & 255, row = t & 127, half = t >> 7, wq = warp & 3;
+    uint64_t* full = bars + g * (GRAD_STAGES + 2);
+    uint64_t *done1 = full + GRAD_STAGES, *done2 = done1 + 1;
+    float2* rowv = reinterpret_cast<float2*>(sm + GRAD_ROW) + g * 128;
+    uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX) + g * 4;
+
+    pdl_trigger();
+    if (warp == 0) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
     }
-}
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < GRAD_GROUPS * (GRAD_STAGES + 2); ++k) mbar_init(bars + k, 1);
+        fence_mbar_init();
+    }
+    float* cst = reinterpret_cast<float*>(sm + GRAD_CST);
+    if (threadIdx.x < HP) cst[threadIdx.x] = threadIdx.x < a.H ? __ldg(a.c1 + threadIdx.x) * LOG2EF : 0.f;
+    const float down = stage_r1(a, sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
+    // dc2: g_r times its atoms, over this CTA's share of the replicas
+    double seeds = 0.0;
+    for (int r = blockIdx.x * GRAD_THREADS + threadIdx.x; r < a.R; r += gridDim.x * GRAD_THREADS) {
+        const int count = off_at(a, r + 1) - off_at(a, r);
+        const float gr = __ldg(a.gE + r);
+        if (count > 0 && gr != 0.f) seeds += (double)gr * count;
+    }
+    for (int o = 16; o > 0; o >>= 1) seeds += __shfl_xor_sync(0xffffffffu, seeds, o);
+    double* wsum = reinterpret_cast<double*>(sm + GRAD_SUM);
+    if (lane == 0) wsum[warp] = seeds;
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0) {
+        seeds = 0.0;
+        for (int w = 0; w < GRAD_THREADS / 32; ++w) seeds += wsum[w];
+        a.part2[blockIdx.x] = seeds;
+    }
 
-// ---------------------------------------------------------------------------
-// readout weight gradients
-// ---------------------------------------------------------------------------
-constexpr int GRAD_CTA = 148;
+    const uint32_t tmem = *tslot + 256 * g;                       // A: 64 columns, D1: 64, D2: 128
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t base = smem_u32(sm) + g * GRAD_GROUP;
+    const uint32_t xrow = base + GRAD_X + row * 16, brow = base + GRAD_B + row * 16;
+    const int ntiles = (a.n + 127) / 128, gid = blockIdx.x + gridDim.x * g;
+    const int first = gid < a.ngroups ? (int)((long long)ntiles * gid / a.ngroups) : 0;
+    const int nt = gid < a.ngroups ? (int)((long long)ntiles * (gid + 1) / a.ngroups) - first : 0;
+    auto row0 = [&](int it) { return (first + it) * 128; };
+    const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
+    const uint64_t rhi = smem_desc(smem_u32(sm) + GRAD_R1, HP * 16, 128);
+    const uint64_t rlo = smem_desc(smem_u32(sm) + GRAD_R1 + R1_TERM, HP * 16, 128);
+    const uint64_t xd = smem_desc(base + GRAD_X, 128, 2048), bd = smem_desc(base + GRAD_B, 128, 2048);
+    float* part = a.part + (size_t)gid * PART;
+    bool ok = true;
 
-// Tile by tile: stage x, form the hidden layer again, stage dp and g ssp(p), then every
-// thread adds its entries of x^T dp.  One partial per CTA, summed in a fixed order.
-__global__ void __launch_bounds__(RT) k_readout_grad(ReadoutArgs a)
-{
-    extern __shared__ float rsm[];
-    float* xs = rsm;                               // [RTILE][F]
-    float* w = xs + RTILE * a.F;                   // [F][H]
-    float* dp = w + a.F * a.H;                     // [RTILE][H]
-    float* ga = dp + RTILE * a.H;                  // [RTILE][H]
-    __shared__ float g[RTILE];
-    for (int k = threadIdx.x; k < a.F * a.H; k += RT) w[k] = a.R1[k];
-    constexpr int MAXE = FP * HP / RT;
-    float acc[MAXE], col = 0.f;
+    if (nt > 0) {
+        if (t == 0)
+            for (int it = 0; it < GRAD_STAGES && it < nt; ++it) tma_tile(base + it * TILE_BYTES, &map, row0(it), full + it);
+        float acc1[32], acc2[32];                                 // this thread's columns half * 32 + k
+        double sum1 = 0.0, sum2 = 0.0;                            // this lane's column, folded
 #pragma unroll
-    for (int k = 0; k < MAXE; ++k) acc[k] = 0.f;
-    double gsum = 0.0;
-    for (int i0 = blockIdx.x * RTILE; i0 < a.n; i0 += gridDim.x * RTILE) {
-        __syncthreads();
-        stage_features(a, i0, xs);
-        if (threadIdx.x < RTILE) {
-            const int i = i0 + threadIdx.x;
-            const int r = i < a.n ? replica_of(a, i) : -1;
-            g[threadIdx.x] = r >= 0 ? a.gE[r] : 0.f;
-            gsum += (double)g[threadIdx.x];
-        }
-        __syncthreads();
-        for (int k = threadIdx.x; k < RTILE * a.H; k += RT) {
-            const int i = k / a.H, h = k % a.H;
-            float p = a.c1[h];
-            for (int f = 0; f < a.F; ++f) p = fmaf(xs[i * a.F + f], w[f * a.H + h], p);
-            const bool in = g[i] != 0.f;           // an atom of no replica adds nothing, whatever it holds
-            dp[k] = in ? g[i] * a.R2[h] * sigmoidf(p) : 0.f;
-            ga[k] = in ? g[i] * ssp(p) : 0.f;
-        }
-        __syncthreads();
+        for (int k = 0; k < 32; ++k) acc1[k] = acc2[k] = 0.f;
+        int E = 120, held = 0, folded = 0;
+        bool emptied = false;
+        int rep = -1;
+        const int end = off_at(a, a.R), begin = off_at(a, 0);
+
+        // D2 2^-E into the group's sums (the MMAs that wrote it have completed)
+        auto flush = [&]() {
+            const float un = __uint_as_float((uint32_t)(127 - E) << 23);
 #pragma unroll
-        for (int k = 0; k < MAXE; ++k) {
-            const int e = threadIdx.x + k * RT;
-            if (e < a.F * a.H) {
-                const int f = e / a.H, h = e % a.H;
-                for (int i = 0; i < RTILE; ++i)
-                    if (g[i] != 0.f) acc[k] = fmaf(xs[i * a.F + f], dp[i * a.H + h], acc[k]);
+            for (int q = 0; q < 2; ++q) {
+                float hi[16], lo[16];
+                tmem_ld16(tmem + lanes + 128 + half * 32 + q * 16, hi);
+                tmem_ld16(tmem + lanes + 192 + half * 32 + q * 16, lo);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float* o = part + (half * 32 + q * 16 + k) * FP + wq * 32 + lane;
+                    const float v = (hi[k] - lo[k]) * un;         // the residual is stored negated
+                    *o = emptied ? *o + v : v;
+                }
+            }
+            emptied = true;
+            held = 0;
+        };
+        auto fold = [&]() {
+            sum1 += (double)fold_columns(acc1);
+            sum2 += (double)fold_columns(acc2);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc1[k] = acc2[k] = 0.f;
+            folded = 0;
+        };
+
+        for (int it = 0; it < nt; ++it) {
+            const int st = it % GRAD_STAGES;
+            // ---- codes -> fp16 in tensor memory (GEMM1's A) and shared memory (GEMM2's A)
+            ok &= mbar_wait_bounded(full + st, (uint32_t)(it / GRAD_STAGES) & 1u, RO_POLLS);
+            __syncwarp();
+            uint32_t v[32];
+            const uint32_t src = base + st * TILE_BYTES + row * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 q = lds128(src + (((half * 4 + c) ^ (row & 7)) << 4));
+                codes_to_half(q.x, v[c * 8 + 0], v[c * 8 + 1]);
+                codes_to_half(q.y, v[c * 8 + 2], v[c * 8 + 3]);
+                codes_to_half(q.z, v[c * 8 + 4], v[c * 8 + 5]);
+                codes_to_half(q.w, v[c * 8 + 6], v[c * 8 + 7]);
+            }
+            tmem_st32(tmem + lanes + half * 32, v);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            if (it > 0) {                                         // GEMM2 of the last tile has read X and B
+                ok &= mbar_wait_bounded(done2, (uint32_t)(it - 1) & 1u, RO_POLLS);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xrow + (half * 8 + c) * 2048), "r"(v[c * 4]),
+                             "r"(v[c * 4 + 1]), "r"(v[c * 4 + 2]), "r"(v[c * 4 + 3])
+                             : "memory");
+            // ---- the row's gradient seed and factor (one half of the threads)
+            if (half == 0) {
+                const int i = row0(it) + row;
+                float gi = 0.f, k = 0.f, m = 0.f;
+                if (i >= begin && i < end) {
+                    rep = advance_replica(a, max(rep, 0), i);
+                    gi = __ldg(a.gE + rep);
+                    if (gi != 0.f) {
+                        const int byte = __ldg(a.scales + i);
+                        k = row_factor(byte, down);
+                        if (k != k) gi = k;                       // NaN scale (or weights): NaN from here on
+                        m = gi * __uint_as_float((uint32_t)byte << 23);
+                    }
+                }
+                rowv[row] = make_float2(gi, k);
+                // the scaled seed's magnitude, finite ones only
+                uint32_t mb = __float_as_uint(m) & 0x7fffffffu;
+                if (mb >= 0x7f800000u) mb = 0;
+                mb = __reduce_max_sync(0xffffffffu, mb);
+                if (lane == 0) gmax[wq] = mb;
+            }
+            tc_fence_before();
+            ok = group_and(1 + g, 256, ok);
+            if (!ok) break;
+            if (t == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < FP / 16; ++ks)
+                    mma_f16_ts(tmem + 64, tmem + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
+#pragma unroll
+                for (int ks = 0; ks < FP / 16; ++ks)
+                    mma_f16_ts(tmem + 64, tmem + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
+                mma_commit(done1);
+                if (it + GRAD_STAGES < nt) tma_tile(base + st * TILE_BYTES, &map, row0(it + GRAD_STAGES), full + st);
+            }
+            __syncwarp();
+            const float2 rv = rowv[row];
+            const uint32_t mb = max(max(gmax[0], gmax[1]), max(gmax[2], gmax[3]));
+            if (mb >= 0x00800000u) {
+                const int e = max(-120, min(120, 13 - ((int)(mb >> 23) - 127)));
+                if (e < E) {
+                    tc_fence_after();
+                    if (held > 0) flush();
+                    E = e;
+                }
+            }
+            if (held >= GRAD_FLUSH) {
+                tc_fence_after();
+                flush();
+            }
+            if (folded >= GRAD_FOLD) fold();
+            const float up = __uint_as_float((uint32_t)(127 + E) << 23);
+            const int i = row0(it) + row;
+            const float gx = rv.x != 0.f ? rv.x * __uint_as_float((uint32_t)__ldg(a.scales + i) << 23) * up : 0.f;
+            ok = mbar_wait_bounded(done1, (uint32_t)it & 1u, RO_POLLS);
+            __syncwarp();
+            tc_fence_after();
+            // ---- epilogue: 16 hidden units at a time
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float d[16];
+                tmem_ld16(tmem + lanes + 64 + half * 32 + q * 16, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {                     // 8 units: one 16-byte piece of each term
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = q * 16 + o * 8 + 2 * j;
+                        const float2 b = *reinterpret_cast<const float2*>(cst + half * 32 + c);
+                        const float2 p = fma2(make_float2(d[o * 8 + 2 * j], d[o * 8 + 2 * j + 1]), dup2(rv.y), b);
+                        const float2 m = make_float2(-fabsf(p.x), -fabsf(p.y));
+                        const float2 u = j % 2 == 0 ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
+                        const float2 hu = mul2(dup2(0.5f), u), y = add2(hu, dup2(0.5f));
+                        const float2 ssp2 = add2(make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)),
+                                                 make_float2(lg2_mufu(y.x), lg2_mufu(y.y)));
+                        const float2 sg = mul2(make_float2(p.x >= 0.f ? 0.5f : hu.x, p.y >= 0.f ? 0.5f : hu.y),
+                                               make_float2(rcp_mufu(y.x), rcp_mufu(y.y)));
+                        const float2 a1 = fma2(dup2(rv.x), sg, make_float2(acc1[c], acc1[c + 1]));
+                        const float2 a2 = fma2(dup2(rv.x), ssp2, make_float2(acc2[c], acc2[c + 1]));
+                        acc1[c] = a1.x; acc1[c + 1] = a1.y;
+                        acc2[c] = a2.x; acc2[c + 1] = a2.y;
+                        const float2 w = mul2(dup2(gx), sg);
+                        split2_neg<0>(w.x, w.y, h[j], l[j]);
+                    }
+                    const uint32_t at = brow + (half * 4 + q * 2 + o) * 2048;
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                                 "r"(h[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 8 * 2048), "r"(l[0]), "r"(l[1]),
+                                 "r"(l[2]), "r"(l[3])
+                                 : "memory");
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            ok = group_and(1 + g, 256, ok);
+            if (!ok) break;
+            if (t == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)                    // 16 atoms a step
+                    mma_f16_ss(tmem + 128, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
+                               held > 0 || ks > 0 ? 1u : 0u);
+                mma_commit(done2);
+            }
+            __syncwarp();
+            ++held;
+            ++folded;
+        }
+        if (ok) ok = mbar_wait_bounded(done2, (uint32_t)(nt - 1) & 1u, RO_POLLS);
+        __syncwarp();
+        if (group_and(1 + g, 256, ok)) {
+            tc_fence_after();
+            flush();
+            fold();
+            double* o = a.colpart + ((size_t)gid * 4 + wq) * 128 + half * 32 + lane;
+            o[0] = sum1;
+            o[64] = sum2;
+        } else {
+            ok = false;
+            if (t == 0) {      // let this group's copies and MMAs in flight end (bounded) before the memory goes
+                for (int st = 0; st < GRAD_STAGES; ++st)
+                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(full + st, ph, 1u << 12);
+                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done1, ph, 1u << 12);
+                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done2, ph, 1u << 12);
             }
         }
-        if (threadIdx.x < 2 * a.H) {
-            const int h = threadIdx.x % a.H;
-            const float* src = threadIdx.x < a.H ? dp : ga;
-            for (int i = 0; i < RTILE; ++i) col += src[i * a.H + h];
-        }
     }
-    float* out = a.part + (size_t)blockIdx.x * (a.F * a.H + 2 * a.H);
-#pragma unroll
-    for (int k = 0; k < MAXE; ++k) {
-        const int e = threadIdx.x + k * RT;
-        if (e < a.F * a.H) out[e] = acc[k];
-    }
-    if (threadIdx.x < 2 * a.H) out[a.F * a.H + threadIdx.x] = col;
-    if (threadIdx.x < 32) {
-        for (int o = 16; o > 0; o >>= 1) gsum += __shfl_xor_sync(0xffffffffu, gsum, o);
-        if (threadIdx.x == 0) a.part2[blockIdx.x] = gsum;
+    tc_fence_before();
+    const int gave_up = __syncthreads_or(!ok);
+    if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up ? 1u : 0u;
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(*tslot, 512);
     }
 }
 
-__global__ void __launch_bounds__(RT) k_readout_grad_sum(ReadoutArgs a, int nparts)
+// dR1 = R2_h sum of the groups' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 sum of g ssp / ln2,
+// dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
+// columns (CTAs 0 .. 4 H - 1: R1, a quarter of the f of one h each; then 4 for c1 and R2;
+// then c2), its 8 warps a share of the partial sums each.
+__global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
 {
-    const int fh = a.F * a.H, m = fh + 2 * a.H;
-    const int k = blockIdx.x * RT + threadIdx.x;
-    if (k < m) {
-        double s = 0.0;
-        for (int c = 0; c < nparts; ++c) s += (double)a.part[(size_t)c * m + k];
-        if (k < fh) a.dR1[k] = (float)s;
-        else if (k < fh + a.H) a.dc1[k - fh] = (float)s;
-        else a.dR2[k - fh - a.H] = (float)s;
-    } else if (k == m) {
-        double s = 0.0;
-        for (int c = 0; c < nparts; ++c) s += a.part2[c];
-        a.dc2[0] = (float)s;
+    pdl_wait();
+    __shared__ double red[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = blockIdx.x;
+    uint32_t bad = 0;
+    for (int k = threadIdx.x; k < a.ncta; k += 256) bad |= a.status[k];
+    bad = __syncthreads_or((int)bad);
+    double s = 0.0;
+    const int nb = 4 * a.H;
+    if (b < nb) {
+        const float* p = a.part + (b >> 2) * FP + (b & 3) * 32 + lane;
+#pragma unroll 8
+        for (int k = w; k < a.ngroups; k += 8) s += (double)p[(size_t)k * PART];
+    } else if (b < nb + 4) {
+        const double* p = a.colpart + (b - nb) * 32 + lane;
+#pragma unroll 8
+        for (int k = w; k < a.ngroups * 4; k += 8) s += p[(size_t)k * 128];
+    } else {
+        for (int k = threadIdx.x; k < a.ncta; k += 256) s += a.part2[k];
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    if (w != 0) return;
+    s = 0.0;
+    for (int k = 0; k < 8; ++k) s += red[k][lane];
+    if (bad) s = (double)__int_as_float(0x7fffffff);
+    if (b < nb) {
+        const int h = b >> 2, f = (b & 3) * 32 + lane;
+        if (f < a.F) a.dR1[f * a.H + h] = (float)(s * (double)a.R2[h]);
+    } else if (b < nb + 4) {
+        const int c = (b - nb) * 32 + lane, h = c & 63;
+        if (h < a.H) {
+            if (c < 64) a.dc1[h] = (float)(s * (double)a.R2[h]);
+            else a.dR2[h] = (float)(s * 0.69314718055994530942);
+        }
+    } else {
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) a.dc2[0] = (float)s;
     }
 }
 
@@ -601,9 +883,9 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
 {
     if (!bytes || n_atoms < 0) return SCHNET_ERR_INVALID_ARG;
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
-    const size_t H = n_features / 2;
-    *bytes = std::max(GRAD_CTA * (sizeof(double) + sizeof(float) * (n_features * H + 2 * H)) + 512,
-                      sizeof(uint32_t) * MAX_SM + sizeof(double) * (((size_t)n_atoms + 31) / 32));
+    const size_t tiles = ((size_t)n_atoms + 127) / 128, groups = std::min<size_t>(tiles, GRAD_GROUPS * MAX_SM);
+    *bytes = (sizeof(uint32_t) + sizeof(double)) * MAX_SM + std::max(sizeof(double) * 4 * tiles,
+                                                  groups * (sizeof(float) * PART + sizeof(double) * 4 * 128));
     return SCHNET_OK;
 }
 
@@ -655,14 +937,21 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     if (cudaPeekAtLastError() != cudaSuccess) return SCHNET_ERR_CUDA;
     a.gE = d_grad_energy;
     a.dR1 = d_dR1; a.dc1 = d_dc1; a.dR2 = d_dR2; a.dc2 = d_dc2;
-    a.part2 = (double*)d_workspace;
-    a.part = (float*)(a.part2 + GRAD_CTA);
+    const int ntiles = (a.n + 127) / 128, nsm = sm_count();
+    a.ngroups = std::min(ntiles, GRAD_GROUPS * nsm);
+    a.ncta = std::min(ntiles, nsm);
+    a.status = (uint32_t*)d_workspace;
+    a.part2 = (double*)(a.status + MAX_SM);
+    a.colpart = a.part2 + MAX_SM;
+    a.part = (float*)(a.colpart + (size_t)a.ngroups * 4 * 128);
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    const size_t smem = sizeof(float) * (RTILE * a.F + a.F * a.H + 2 * RTILE * a.H);
-    if (cudaFuncSetAttribute(k_readout_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SCHNET_ERR_CUDA;
-    const int grid = std::max(1, std::min((a.n + RTILE - 1) / RTILE, GRAD_CTA));
-    k_readout_grad<<<grid, RT, smem, s>>>(a);
-    k_readout_grad_sum<<<(a.F * a.H + 2 * a.H + RT) / RT, RT, 0, s>>>(a, grid);
+    if (a.n > 0) {
+        CUtensorMap map;
+        if (!code_map(a, &map) || cudaFuncSetAttribute(k_readout_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)GRAD_SMEM) != cudaSuccess)
+            return SCHNET_ERR_CUDA;
+        k_readout_grad<<<a.ncta, GRAD_THREADS, GRAD_SMEM, s>>>(map, a);
+    }
+    if (launch_pdl(k_readout_grad_sum, 4 * a.H + 5, 256, 0, s, a) != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
 }
