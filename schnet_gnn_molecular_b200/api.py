@@ -7,6 +7,7 @@ memory (the workspace is one uint8 tensor) and the stream.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import numpy as np
 import torch
@@ -200,91 +201,103 @@ def feature_width(F: int) -> int:
     return (F + 15) // 16 * 16
 
 
-def _require(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _call(device, fn, *args):
-    """fn(*args, stream) with the tensors' device current and its current stream."""
-    with torch.cuda.device(device):
-        st = fn(*args, C.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+def _call(fn, device, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, _raw_stream(i))
     if st != nat.OK:
         raise SchNetError(st, fn.__name__)
 
 
-def _scratch(device, size_fn, *args):
-    """A workspace of the bytes that size_fn names, from the caching allocator (so calls on different
-    streams, or captured into different graphs, never share one)."""
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(name, *args):
     n = C.c_size_t(0)
-    with torch.cuda.device(device):
-        st = size_fn(*args, C.byref(n))
+    st = getattr(nat.load(), name)(*args, C.byref(n))
     if st != nat.OK:
-        raise SchNetError(st, size_fn.__name__)
-    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+        raise SchNetError(st, name)
+    return int(n.value)
+
+
+def _scratch(like, name, *args):
+    """A workspace on `like`'s device of the bytes that the library call `name` asks for, from the caching allocator
+    (so calls on different streams, or captured into different graphs, never share one)."""
+    n = _scratch_bytes(name, *args)
+    return like.new_empty(n, dtype=torch.uint8), n
+
+
+def _check_tensor(t, dev, name, dtype, shape):
+    """t: a contiguous tensor on dev of that dtype (None: any of one byte) and shape (None: any)."""
+    if (t.device != dev or not t.is_contiguous() or (t.dtype != dtype if dtype is not None else t.element_size() != 1)
+            or (shape is not None and t.shape != shape)):
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype or 'bytes'} on {dev}"
+                         f"{'' if shape is None else f' of shape {tuple(shape)}'}; got {t.dtype} {tuple(t.shape)}")
 
 
 def store_features(x: torch.Tensor):
     """(codes, scales) of the rows of x [n, F] (float32, float16 or bfloat16; unit column stride): e4m3 codes
     [n, feature_width(F)] (zeros past F) and one power-of-two scale a row [n]; the stored value is
     codes.float()[:, :F] * scales.float()[:, None].  See schnet_store_features in include/schnet.h."""
-    _require(x.is_cuda and x.dim() == 2, "store_features: x must be a 2-d CUDA tensor")
-    _require(x.dtype in _STORE_DTYPES, f"store_features: dtype {x.dtype}")
+    dtype = _STORE_DTYPES.get(x.dtype)
+    if not x.is_cuda or x.dim() != 2 or dtype is None:
+        raise ValueError("store_features: x must be a 2-d float32, float16 or bfloat16 CUDA tensor")
     n, F = x.shape
-    _require(n == 0 or (x.stride(1) == 1 and (n == 1 or x.stride(0) >= F)),
-             "store_features: columns must be adjacent and rows must not overlap")
-    codes = torch.empty((n, feature_width(F)), dtype=torch.float8_e4m3fn, device=x.device)
-    scales = torch.empty(n, dtype=torch.float8_e8m0fnu, device=x.device)
-    _call(x.device, nat.load().schnet_store_features, _ptr(x), _STORE_DTYPES[x.dtype], n, F, max(x.stride(0), F),
-          _ptr(codes), _ptr(scales))
+    stride, unit = x.stride()
+    if n > 0 and (unit != 1 or (n > 1 and stride < F)):
+        raise ValueError("store_features: columns must be adjacent and rows must not overlap")
+    codes = x.new_empty((n, feature_width(F)), dtype=torch.float8_e4m3fn)
+    scales = x.new_empty(n, dtype=torch.float8_e8m0fnu)
+    _call(nat.load().schnet_store_features, x.device, x.data_ptr(), dtype, n, F, max(stride, F), codes.data_ptr(),
+          scales.data_ptr())
     return codes, scales
 
 
 def _readout_args(codes, scales, replica_offsets, readout):
     dev = codes.device
-    R1, c1, R2, c2 = (readout[k] for k in ("R1", "c1", "R2", "c2"))
-    for k, t in (("codes", codes), ("scales", scales), ("replica_offsets", replica_offsets), ("R1", R1), ("c1", c1),
-                 ("R2", R2), ("c2", c2)):
-        _require(t.is_cuda and t.device == dev and t.is_contiguous(), f"{k} must be a contiguous tensor on {dev}")
-    for k, t in (("R1", R1), ("c1", c1), ("R2", R2), ("c2", c2)):
-        _require(t.dtype == torch.float32, f"{k} must be float32")
-    _require(R1.dim() == 2 and R1.shape[0] == 2 * R1.shape[1], f"R1 must be [F, F / 2], is {tuple(R1.shape)}")
+    R1, c1, R2, c2 = readout["R1"], readout["c1"], readout["R2"], readout["c2"]
+    if not codes.is_cuda or codes.dim() != 2 or R1.dim() != 2 or replica_offsets.dim() != 1:
+        raise ValueError("codes [n, width], R1 [F, F / 2] and replica_offsets [R + 1] must be CUDA tensors")
     F, H = R1.shape
-    _require(c1.shape == (H,) and R2.shape == (H,) and c2.numel() == 1, "c1, R2 must be [F / 2] and c2 one value")
-    _require(codes.dim() == 2 and codes.shape[1] == feature_width(F) and codes.element_size() == 1,
-             f"codes must be [n, {feature_width(F)}] bytes")
-    n = codes.shape[0]
-    _require(scales.shape == (n,) and scales.element_size() == 1, "scales must be [n] bytes")
-    _require(replica_offsets.dim() == 1 and replica_offsets.numel() >= 2 and replica_offsets.dtype == torch.int32,
-             "replica_offsets must be int32 [R + 1]")
-    _require(n < 2 ** 31, "too many atoms")
+    n, R = codes.shape[0], replica_offsets.shape[0] - 1
+    if F != 2 * H or R < 1 or n >= 2 ** 31 or c2.numel() != 1:
+        raise ValueError(f"R1 must be [F, F / 2], is {(F, H)}; replica_offsets [R + 1] with R >= 1; c2 one value; "
+                         "fewer than 2^31 atoms")
+    _check_tensor(codes, dev, "codes", None, (n, feature_width(F)))
+    _check_tensor(scales, dev, "scales", None, (n,))
+    _check_tensor(replica_offsets, dev, "replica_offsets", torch.int32, None)
+    _check_tensor(R1, dev, "R1", torch.float32, None)
+    _check_tensor(c1, dev, "c1", torch.float32, (H,))
+    _check_tensor(R2, dev, "R2", torch.float32, (H,))
+    _check_tensor(c2, dev, "c2", torch.float32, None)
     w = nat.Readout(R1.data_ptr(), c1.data_ptr(), R2.data_ptr(), c2.data_ptr())
-    ws = _scratch(dev, nat.load().schnet_readout_workspace_bytes, n, F)
-    R = replica_offsets.numel() - 1
-    return dev, F, H, R, ws, (_ptr(codes), _ptr(scales), n, F, R, _ptr(replica_offsets), C.byref(w))
+    ws, size = _scratch(codes, "schnet_readout_workspace_bytes", n, F)
+    return dev, n, F, R, ws, size, (codes.data_ptr(), scales.data_ptr(), n, F, R, replica_offsets.data_ptr(),
+                                    C.byref(w))
 
 
 def readout_energy(codes, scales, replica_offsets, readout):
     """(energy [R], eps [n]) float32: readout energies from stored features.  replica_offsets int32 [R + 1] on the
     device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
-    dev, _, _, R, ws, args = _readout_args(codes, scales, replica_offsets, readout)
-    energy = torch.empty(R, dtype=torch.float32, device=dev)
-    eps = torch.empty(codes.shape[0], dtype=torch.float32, device=dev)
-    _call(dev, nat.load().schnet_readout_energy, *args, _ptr(energy), _ptr(eps), _ptr(ws), ws.numel())
+    dev, n, _, R, ws, size, args = _readout_args(codes, scales, replica_offsets, readout)
+    energy, eps = readout["R1"].new_empty(R), readout["R1"].new_empty(n)
+    _call(nat.load().schnet_readout_energy, dev, *args, energy.data_ptr(), eps.data_ptr(), ws.data_ptr(), size)
     return energy, eps
 
 
 def readout_gradients(codes, scales, replica_offsets, readout, grad_energy):
     """{"R1", "c1", "R2", "c2"}: gradients of sum_r grad_energy[r] E_r with respect to the readout's weights, from
     stored features; grad_energy float32 [R] (e.g. the third result of preference_loss)."""
-    dev, F, H, R, ws, args = _readout_args(codes, scales, replica_offsets, readout)
-    _require(grad_energy.device == dev and grad_energy.dtype == torch.float32 and grad_energy.shape == (R,)
-             and grad_energy.is_contiguous(), f"grad_energy must be contiguous float32 [{R}] on {dev}")
-    out = {k: torch.empty(s, dtype=torch.float32, device=dev) for k, s in
-           (("R1", (F, H)), ("c1", (H,)), ("R2", (H,)), ("c2", (1,)))}
-    _call(dev, nat.load().schnet_readout_gradients, *args, _ptr(grad_energy), *(_ptr(out[k]) for k in out), _ptr(ws),
-          ws.numel())
-    return out
+    dev, _, F, R, ws, size, args = _readout_args(codes, scales, replica_offsets, readout)
+    _check_tensor(grad_energy, dev, "grad_energy", torch.float32, (R,))
+    H = F // 2
+    new = grad_energy.new_empty
+    d1, d2, d3, d4 = new((F, H)), new(H), new(H), new(1)
+    _call(nat.load().schnet_readout_gradients, dev, *args, grad_energy.data_ptr(), d1.data_ptr(), d2.data_ptr(),
+          d3.data_ptr(), d4.data_ptr(), ws.data_ptr(), size)
+    return {"R1": d1, "c1": d2, "R2": d3, "c2": d4}
 
 
 def preference_loss(energy, pairs, *, kT, reference=None, smoothing=0.0, flags=None):
@@ -293,27 +306,26 @@ def preference_loss(energy, pairs, *, kT, reference=None, smoothing=0.0, flags=N
     float64 [R]; kT in the energies' unit; flags: optional int32 [1] tensor that receives the SCHNET_FLAG_* bits of
     this call.  See schnet_preference_loss in include/schnet.h."""
     dev = energy.device
-    _require(energy.is_cuda and energy.dim() == 1 and energy.numel() >= 1 and energy.is_contiguous()
-             and energy.dtype in _ENERGY_DTYPES, "energy must be a contiguous float32 or float64 CUDA tensor [R]")
+    dtype = _ENERGY_DTYPES.get(energy.dtype)
+    if not energy.is_cuda or energy.dim() != 1 or energy.shape[0] < 1 or dtype is None or not energy.is_contiguous():
+        raise ValueError("energy must be a contiguous float32 or float64 CUDA tensor [R]")
+    R, P = energy.shape[0], pairs.shape[0]
     if reference is not None:
-        _require(reference.device == dev and reference.dtype == energy.dtype and reference.shape == energy.shape
-                 and reference.is_contiguous(), "reference must be like energy")
-    _require(pairs.device == dev and pairs.dtype == torch.int32 and pairs.dim() == 2 and pairs.shape[1] == 2
-             and pairs.is_contiguous(), "pairs must be contiguous int32 [P, 2] on the energies' device")
-    _require(flags is None or (flags.device == dev and flags.numel() == 1 and flags.element_size() == 4),
-             "flags must be one 32-bit integer on the energies' device")
-    R, P = energy.numel(), pairs.shape[0]
-    lib = nat.load()
-    ws = _scratch(dev, lib.schnet_preference_workspace_bytes, R, P)
-    loss = torch.empty((), dtype=torch.float64, device=dev)
-    margins = torch.empty(P, dtype=torch.float32, device=dev)
-    grad = torch.empty(R, dtype=torch.float32, device=dev)
-    _call(dev, lib.schnet_preference_loss, _ptr(energy), _ptr(reference), _ENERGY_DTYPES[energy.dtype], R,
-          _ptr(pairs), P, float(kT), float(smoothing), _ptr(loss), _ptr(margins), _ptr(grad), _ptr(flags), _ptr(ws),
-          ws.numel())
+        _check_tensor(reference, dev, "reference", energy.dtype, energy.shape)
+    _check_tensor(pairs, dev, "pairs", torch.int32, (P, 2))
+    if flags is not None and (flags.device != dev or flags.numel() != 1 or flags.element_size() != 4):
+        raise ValueError("flags must be one 32-bit integer on the energies' device")
+    ws, size = _scratch(pairs, "schnet_preference_workspace_bytes", R, P)
+    loss = energy.new_empty((), dtype=torch.float64)
+    margins, grad = energy.new_empty(P, dtype=torch.float32), energy.new_empty(R, dtype=torch.float32)
+    _call(nat.load().schnet_preference_loss, dev, energy.data_ptr(), reference.data_ptr() if reference is not None else None,
+          dtype, R, pairs.data_ptr(), P, kT, smoothing, loss.data_ptr(), margins.data_ptr(), grad.data_ptr(),
+          flags.data_ptr() if flags is not None else None, ws.data_ptr(), size)
     return loss, margins, grad
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda i: torch.cuda.current_stream(i).cuda_stream
 _STORE_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _ENERGY_DTYPES = {torch.float32: 0, torch.float64: 3}
 

@@ -6,6 +6,7 @@
 // x / scale is exact and the e4m3 rounding is the only one: codes are a function of
 // x alone, whatever computes them.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -191,27 +192,37 @@ __device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
 // Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the epilogues' exponentials
 // do not all keep a NaN).  All threads of the CTA; red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
+template <int THREADS>
 __device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, uint32_t* red)
 {
-    uint32_t mx = 0;                     // as bits, which order like the magnitudes
-    const int total = a.F * a.H;
-    for (int k = threadIdx.x; k < total; k += blockDim.x) mx = max(mx, __float_as_uint(__ldg(a.R1 + k)) & 0x7fffffffu);
+    constexpr int PAIRS = HP * FP / 2 / THREADS;                // (f, f + 1) of one hidden unit each
+    float v[PAIRS][2];
+    uint32_t mx = 0;                                            // as bits, which order like the magnitudes
     if (threadIdx.x < a.H && (__float_as_uint(__ldg(a.c1 + threadIdx.x)) & 0x7fffffffu) >= 0x7f800000u) mx = 0x7f800000u;
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+        const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            v[j][u] = h < a.H && f + u < a.F ? __ldg(a.R1 + (f + u) * a.H + h) : 0.f;
+            mx = max(mx, __float_as_uint(v[j][u]) & 0x7fffffffu);
+        }
+    }
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
     __syncthreads();
     mx = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) mx = max(mx, red[w]);
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) mx = max(mx, red[w]);
     const int ex = (int)(mx >> 23);
     int s = ex > 0 && ex < 255 ? 14 - (ex - 127) : 0;
     s = max(-110, min(110, s));
     const float up = __uint_as_float((uint32_t)(127 + s) << 23);
-    for (int k = threadIdx.x; k < HP * FP / 2; k += blockDim.x) {
-        const int h = k % HP, f = k / HP * 2;                   // two inputs of one hidden unit
-        const float v0 = h < a.H && f < a.F ? __ldg(a.R1 + f * a.H + h) * up : 0.f;
-        const float v1 = h < a.H && f + 1 < a.F ? __ldg(a.R1 + (f + 1) * a.H + h) * up : 0.f;
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+        const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
         uint32_t vh, vl;
-        split2<0>(v0, v1, vh, vl);
+        split2<0>(v[j][0] * up, v[j][1] * up, vh, vl);
         *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
         *reinterpret_cast<uint32_t*>(lo + kmajor_off(h, f, HP)) = vl;
     }
@@ -257,9 +268,14 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < FWD_GROUPS * (FWD_STAGES + 1); ++k) mbar_init(bars + k, 1);
+    const uint32_t stage0 = smem_u32(sm) + FWD_STAGE0 + g * FWD_STAGES * TILE_BYTES;
+    const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x, gid = blockIdx.x + gridDim.x * g;
+    const int nt = gid < ntiles ? (ntiles - gid + ngroups - 1) / ngroups : 0;
+    auto row0 = [&](int it) { return (gid + it * ngroups) * 128; };
+    if (t == 0) {                                                 // the first tiles are on their way before R1 is read
+        for (int k = 0; k <= FWD_STAGES; ++k) mbar_init(full + k, 1);
         fence_mbar_init();
+        for (int it = 0; it < FWD_STAGES && it < nt; ++it) tma_tile(stage0 + it * TILE_BYTES, &map, row0(it), full + it);
     }
     if (threadIdx.x < 32) {
         const int h = threadIdx.x * 2;
@@ -267,7 +283,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         cst[threadIdx.x] = make_float4(i0 ? __ldg(a.c1 + h) * LOG2EF : 0.f, i1 ? __ldg(a.c1 + h + 1) * LOG2EF : 0.f,
                                        i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
     }
-    const float down = stage_r1(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
+    const float down = stage_r1<FWD_THREADS>(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
     const float c2 = __ldg(a.c2);
     fence_proxy_async_smem();
     tc_fence_before();
@@ -276,10 +292,6 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 
     const uint32_t tmem = *tslot + 128 * g;                       // A: 64 columns, D: 64 columns
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t stage0 = smem_u32(sm) + FWD_STAGE0 + g * FWD_STAGES * TILE_BYTES;
-    const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x, gid = blockIdx.x + gridDim.x * g;
-    const int nt = gid < ntiles ? (ntiles - gid + ngroups - 1) / ngroups : 0;
-    auto row0 = [&](int it) { return (gid + it * ngroups) * 128; };
     auto scale_of = [&](int it) { return it < nt && row0(it) + t < a.n ? (int)__ldg(a.scales + row0(it) + t) : 127; };
     const uint32_t id = idesc_f16(128, HP, 0, 0);
     const uint64_t bhi = smem_desc(smem_u32(sm) + FWD_R1, HP * 16, 128);
@@ -328,9 +340,6 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     };
 
     if (nt > 0) {
-        if (t == 0)
-            for (int it = 0; it < FWD_STAGES && it < nt; ++it)
-                tma_tile(stage0 + it * TILE_BYTES, &map, row0(it), full + it);
         int byte = scale_of(0);
         widen(0);
         start(0);
@@ -519,13 +528,19 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < GRAD_GROUPS * (GRAD_STAGES + 2); ++k) mbar_init(bars + k, 1);
+    const uint32_t base = smem_u32(sm) + g * GRAD_GROUP;
+    const int ntiles = (a.n + 127) / 128, gid = blockIdx.x + gridDim.x * g;
+    const int first = gid < a.ngroups ? (int)((long long)ntiles * gid / a.ngroups) : 0;
+    const int nt = gid < a.ngroups ? (int)((long long)ntiles * (gid + 1) / a.ngroups) - first : 0;
+    auto row0 = [&](int it) { return (first + it) * 128; };
+    if (t == 0) {                                                 // the first tiles are on their way before R1 is read
+        for (int k = 0; k < GRAD_STAGES + 2; ++k) mbar_init(full + k, 1);
         fence_mbar_init();
+        for (int it = 0; it < GRAD_STAGES && it < nt; ++it) tma_tile(base + it * TILE_BYTES, &map, row0(it), full + it);
     }
     float* cst = reinterpret_cast<float*>(sm + GRAD_CST);
     if (threadIdx.x < HP) cst[threadIdx.x] = threadIdx.x < a.H ? __ldg(a.c1 + threadIdx.x) * LOG2EF : 0.f;
-    const float down = stage_r1(a, sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
+    const float down = stage_r1<GRAD_THREADS>(a, sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
     // dc2: g_r times its atoms, over this CTA's share of the replicas
     double seeds = 0.0;
     for (int r = blockIdx.x * GRAD_THREADS + threadIdx.x; r < a.R; r += gridDim.x * GRAD_THREADS) {
@@ -548,12 +563,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 
     const uint32_t tmem = *tslot + 256 * g;                       // A: 64 columns, D1: 64, D2: 128
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t base = smem_u32(sm) + g * GRAD_GROUP;
     const uint32_t xrow = base + GRAD_X + row * 16, brow = base + GRAD_B + row * 16;
-    const int ntiles = (a.n + 127) / 128, gid = blockIdx.x + gridDim.x * g;
-    const int first = gid < a.ngroups ? (int)((long long)ntiles * gid / a.ngroups) : 0;
-    const int nt = gid < a.ngroups ? (int)((long long)ntiles * (gid + 1) / a.ngroups) - first : 0;
-    auto row0 = [&](int it) { return (first + it) * 128; };
     const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
     const uint64_t rhi = smem_desc(smem_u32(sm) + GRAD_R1, HP * 16, 128);
     const uint64_t rlo = smem_desc(smem_u32(sm) + GRAD_R1 + R1_TERM, HP * 16, 128);
@@ -562,8 +572,6 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     bool ok = true;
 
     if (nt > 0) {
-        if (t == 0)
-            for (int it = 0; it < GRAD_STAGES && it < nt; ++it) tma_tile(base + it * TILE_BYTES, &map, row0(it), full + it);
         float acc1[32], acc2[32];                                 // this thread's columns half * 32 + k
         double sum1 = 0.0, sum2 = 0.0;                            // this lane's column, folded
 #pragma unroll
@@ -820,6 +828,18 @@ static int sm_count()
     return std::min(n, MAX_SM);
 }
 
+// more than 48 KB of shared memory for a kernel, once per device
+static bool allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& set)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && (set.load() >> dev & 1)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    if (dev < 64) set.fetch_or((uint64_t)1 << dev);
+    return true;
+}
+static std::atomic<uint64_t> g_fwd_set{0}, g_grad_set{0};
+
 // tensor map of the codes: rows of W bytes, boxes of 128 rows x 128 bytes, 128-byte swizzle
 static bool code_map(const ReadoutArgs& a, CUtensorMap* map)
 {
@@ -910,8 +930,7 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
     a.csum = (double*)(a.status + MAX_SM);
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || cudaFuncSetAttribute(k_readout_eps, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)FWD_SMEM) != cudaSuccess)
+        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, g_fwd_set))
             return SCHNET_ERR_CUDA;
         k_readout_eps<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
     }
@@ -947,8 +966,7 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || cudaFuncSetAttribute(k_readout_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)GRAD_SMEM) != cudaSuccess)
+        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_grad, GRAD_SMEM, g_grad_set))
             return SCHNET_ERR_CUDA;
         k_readout_grad<<<a.ncta, GRAD_THREADS, GRAD_SMEM, s>>>(map, a);
     }
