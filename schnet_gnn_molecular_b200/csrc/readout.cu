@@ -166,6 +166,49 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     return v;
 }
 
+// 16 consecutive 32-bit TMEM columns of this warp's 32 lanes <- 16 registers per thread
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// One lane of a converged warp.  The MMAs below are issued by a whole warp with a predicate
+// from here and warp-uniform operands: behind a branch on the thread index the compiler
+// moves every operand to a uniform register anew, which costs 60-130 cycles an MMA against 20.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p;
+}
+
+// D[tmem] (+)= A[tmem] B[smem desc] and D[tmem] (+)= A[smem desc] B[smem desc], kind::f16,
+// by the lane with go != 0
+__device__ __forceinline__ void mma_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc), "r"(go)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc), "r"(go)
+                 : "memory");
+}
+
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -195,7 +238,7 @@ constexpr uint32_t R1_TERM = HP * FP * 2;
 template <int THREADS>
 __device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, uint32_t* red)
 {
-    constexpr int PAIRS = HP * FP / 2 / THREADS;                // (f, f + 1) of one hidden unit each
+    constexpr int PAIRS = (HP * FP / 2 + THREADS - 1) / THREADS;   // (f, f + 1) of one hidden unit each
     float v[PAIRS][2];
     uint32_t mx = 0;                                            // as bits, which order like the magnitudes
     if (threadIdx.x < a.H && (__float_as_uint(__ldg(a.c1 + threadIdx.x)) & 0x7fffffffu) >= 0x7f800000u) mx = 0x7f800000u;
@@ -221,6 +264,7 @@ __device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uin
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
         const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
+        if (k >= HP * FP / 2) break;
         uint32_t vh, vl;
         split2<0>(v[j][0] * up, v[j][1] * up, vh, vl);
         *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
@@ -236,46 +280,55 @@ __device__ __forceinline__ float row_factor(int byte, float down)
     return fminf(__uint_as_float((uint32_t)byte << 23) * down, 1e38f) * LOG2EF;
 }
 
-// Energies.  Four groups of 4 warps share the CTA's R1; each takes every (4 gridDim)-th
-// tile of 128 atoms, one atom per thread: its row of codes is read from the TMA stage,
-// widened to fp16 (exact) and put into tensor memory as the MMA's A operand (lane = atom),
-// so D[atom][h] = codes . R1 comes back with a whole hidden layer per thread and the sum
-// over h needs no exchange.  The next tile's MMAs run under this tile's epilogue.
-// Bound: the 2 transcendentals per hidden unit (MUFU: 8 cycles an atom and SM) and HBM
-// (133 bytes: 5.9 cycles); three quarters of the exponentials go to the FMA pipe.
-constexpr int FWD_GROUPS = 4, FWD_STAGES = 2, FWD_THREADS = FWD_GROUPS * 128;
-constexpr uint32_t FWD_STAGE0 = 0;
+// Energies.  Four groups of 4 warps and one issuing warp share the CTA's R1.  A group takes
+// every (4 gridDim)-th tile of 128 atoms, one atom per thread: its row of codes is read from
+// the TMA stage, widened to fp16 (exact) and put into tensor memory as the MMA's A operand
+// (lane = atom), so D[atom][h] = codes . R1 comes back with a whole hidden layer per thread
+// and the sum over h needs no exchange.  A group widens tile it+1, reads D(it) into registers,
+// hands both on to the issuing warp and only then works on D(it), which hides the MMAs.
+// The issuing thread blocks while the tensor core's queue is full, so it does nothing else:
+// a group's own thread that issued held back its group.
+// Bound: the 2 transcendentals per hidden unit (all on the MUFU: 8 cycles an atom and SM)
+// and HBM (133 bytes: 5.9 cycles); FWD_FMA of 8 pairs' exponentials go to the FMA pipe.
+constexpr int FWD_GROUPS = 4, FWD_STAGES = 2, FWD_THREADS = FWD_GROUPS * 128 + 32;
+constexpr int FWD_FMA = 2;
 constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
 constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
 constexpr uint32_t FWD_RED = FWD_CST + 32 * 16;
-constexpr uint32_t FWD_BAR = FWD_RED + 64;
-constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * (FWD_STAGES + 1) + 16 + 1024;
+constexpr uint32_t FWD_BAR = FWD_RED + 128;
+constexpr int FWD_NBAR = FWD_STAGES + 2;                         // per group: stages full, A ready, MMAs done
+constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * FWD_NBAR + 16;
 
 __global__ void __launch_bounds__(FWD_THREADS, 1)
 k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 {
-    extern __shared__ uint8_t raw[];
-    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     float4* cst = reinterpret_cast<float4*>(sm + FWD_CST);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + FWD_BAR);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + FWD_GROUPS * (FWD_STAGES + 1));
-    const int warp = threadIdx.x >> 5, g = threadIdx.x >> 7, t = threadIdx.x & 127;
-    uint64_t* full = bars + g * (FWD_STAGES + 1);
-    uint64_t* done = full + FWD_STAGES;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + FWD_GROUPS * FWD_NBAR);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x;
+    const uint32_t stages = smem_u32(sm);
+    auto tiles_of = [&](int gid) { return gid < ntiles ? (ntiles - gid + ngroups - 1) / ngroups : 0; };
+    auto first_row = [&](int g, int it) { return ((int)blockIdx.x + (int)gridDim.x * g + it * ngroups) * 128; };
 
     pdl_trigger();
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    const uint32_t stage0 = smem_u32(sm) + FWD_STAGE0 + g * FWD_STAGES * TILE_BYTES;
-    const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x, gid = blockIdx.x + gridDim.x * g;
-    const int nt = gid < ntiles ? (ntiles - gid + ngroups - 1) / ngroups : 0;
-    auto row0 = [&](int it) { return (gid + it * ngroups) * 128; };
-    if (t == 0) {                                                 // the first tiles are on their way before R1 is read
-        for (int k = 0; k <= FWD_STAGES; ++k) mbar_init(full + k, 1);
+    if (threadIdx.x == FWD_GROUPS * 128) {                        // the first tiles are on their way before R1 is read
+        for (int g = 0; g < FWD_GROUPS; ++g) {
+            uint64_t* full = bars + g * FWD_NBAR;
+            for (int k = 0; k < FWD_STAGES; ++k) mbar_init(full + k, 1);
+            mbar_init(full + FWD_STAGES, 4);
+            mbar_init(full + FWD_STAGES + 1, 1);
+        }
         fence_mbar_init();
-        for (int it = 0; it < FWD_STAGES && it < nt; ++it) tma_tile(stage0 + it * TILE_BYTES, &map, row0(it), full + it);
+        for (int it = 0; it < FWD_STAGES; ++it)
+            for (int g = 0; g < FWD_GROUPS; ++g)
+                if (it < tiles_of(blockIdx.x + gridDim.x * g))
+                    tma_tile(stages + (g * FWD_STAGES + it) * TILE_BYTES, &map, first_row(g, it), bars + g * FWD_NBAR + it);
     }
     if (threadIdx.x < 32) {
         const int h = threadIdx.x * 2;
@@ -284,106 +337,120 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                                        i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
     }
     const float down = stage_r1<FWD_THREADS>(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
-    const float c2 = __ldg(a.c2);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-
-    const uint32_t tmem = *tslot + 128 * g;                       // A: 64 columns, D: 64 columns
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    auto scale_of = [&](int it) { return it < nt && row0(it) + t < a.n ? (int)__ldg(a.scales + row0(it) + t) : 127; };
-    const uint32_t id = idesc_f16(128, HP, 0, 0);
-    const uint64_t bhi = smem_desc(smem_u32(sm) + FWD_R1, HP * 16, 128);
-    const uint64_t blo = smem_desc(smem_u32(sm) + FWD_R1 + R1_TERM, HP * 16, 128);
     bool ok = true;
 
-    // codes of tile it -> tensor memory
-    auto widen = [&](int it) {
-        const int st = it % FWD_STAGES;
-        ok &= mbar_wait_bounded(full + st, (uint32_t)(it / FWD_STAGES) & 1u, RO_POLLS);
-        __syncwarp();
-        const uint32_t row = stage0 + st * TILE_BYTES + t * 128;
+    if (warp == FWD_GROUPS * 4) {
+        // ---- issuing warp: every group's tiles in turn
+        const uint32_t id = idesc_f16(128, HP, 0, 0);
+        const uint64_t bhi = smem_desc(stages + FWD_R1, HP * 16, 128);
+        const uint64_t blo = smem_desc(stages + FWD_R1 + R1_TERM, HP * 16, 128);
+        const uint32_t tm0 = __shfl_sync(0xffffffffu, *tslot, 0), go = elect_one();
+        const int most = tiles_of(blockIdx.x);
+        for (int it = 0; it < most && ok; ++it)
+            for (int g = 0; g < FWD_GROUPS; ++g) {
+                const int nt = tiles_of(blockIdx.x + gridDim.x * g);
+                if (it >= nt) continue;
+                uint64_t* full = bars + g * FWD_NBAR;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + FWD_STAGES, (uint32_t)it & 1u, RO_POLLS));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tm = tm0 + 128 * g;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
+                for (int ks = 0; ks < FP / 16; ++ks)              // the small terms first
+                    mma_ts(go, tm + 64, tm + ks * 8, blo + (uint64_t)((ks * 2 * HP * 16) >> 4), id, ks > 0 ? 1u : 0u);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 q = lds128(row + (((half * 4 + c) ^ (t & 7)) << 4));
-                codes_to_half(q.x, v[c * 8 + 0], v[c * 8 + 1]);
-                codes_to_half(q.y, v[c * 8 + 2], v[c * 8 + 3]);
-                codes_to_half(q.z, v[c * 8 + 4], v[c * 8 + 5]);
-                codes_to_half(q.w, v[c * 8 + 6], v[c * 8 + 7]);
+                for (int ks = 0; ks < FP / 16; ++ks)
+                    mma_ts(go, tm + 64, tm + ks * 8, bhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id, 1u);
+                if (go) {
+                    mma_commit(full + FWD_STAGES + 1);
+                    const int st = it % FWD_STAGES;               // the group has read this stage
+                    if (it + FWD_STAGES < nt)
+                        tma_tile(stages + (g * FWD_STAGES + st) * TILE_BYTES, &map, first_row(g, it + FWD_STAGES), full + st);
+                }
+                __syncwarp();
             }
-            tmem_st32(tmem + lanes + half * 32, v);
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    };
-    // all of the group's rows are in tensor memory: MMAs of tile it, and the stage's next tile
-    auto start = [&](int it) {
-        tc_fence_before();
-        ok = group_and(1 + g, 128, ok);
-        if (!ok) return;
-        if (t == 0) {
-            tc_fence_after();
+        if (!ok && go)   // a wait gave up: let the copies and MMAs in flight end (bounded) before the memory goes
+            for (int k = 0; k < FWD_GROUPS * FWD_NBAR; ++k)
+                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(bars + k, ph, 1u << 12);
+    } else {
+        const int g = threadIdx.x >> 7, t = threadIdx.x & 127;
+        uint64_t* full = bars + g * FWD_NBAR;
+        const uint32_t tmem = *tslot + 128 * g + ((uint32_t)((warp & 3) * 32) << 16);    // A: 64 columns, D: 64 columns
+        const uint32_t stage0 = stages + g * FWD_STAGES * TILE_BYTES + t * 128;
+        const int nt = tiles_of(blockIdx.x + gridDim.x * g);
+        const float c2 = __ldg(a.c2);
+        auto scale_of = [&](int it) {
+            const int i = first_row(g, it) + t;
+            return it < nt && i < a.n ? (int)__ldg(a.scales + i) : 127;
+        };
+        // codes of tile it -> fp16 in tensor memory, then the issuing warp's turn
+        auto widen = [&](int it) {
+            const int st = it % FWD_STAGES;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + st, (uint32_t)(it / FWD_STAGES) & 1u, RO_POLLS));
+            const uint32_t src = stage0 + st * TILE_BYTES;
 #pragma unroll
-            for (int ks = 0; ks < FP / 16; ++ks)                  // the small terms first
-                mma_f16_ts(tmem + 64, tmem + ks * 8, blo + (uint64_t)((ks * 2 * HP * 16) >> 4), id, ks > 0 ? 1u : 0u);
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v[16];
 #pragma unroll
-            for (int ks = 0; ks < FP / 16; ++ks)
-                mma_f16_ts(tmem + 64, tmem + ks * 8, bhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id, 1u);
-            mma_commit(done);
-            if (it + FWD_STAGES < nt)
-                tma_tile(stage0 + (it % FWD_STAGES) * TILE_BYTES, &map, row0(it + FWD_STAGES), full + it % FWD_STAGES);
-        }
-        __syncwarp();
-    };
-
-    if (nt > 0) {
-        int byte = scale_of(0);
-        widen(0);
-        start(0);
-        for (int it = 0; it < nt && ok; ++it) {
-            const float k = row_factor(byte, down);
-            byte = scale_of(it + 1);
-            ok = mbar_wait_bounded(done, (uint32_t)it & 1u, RO_POLLS);
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 w = lds128(src + (((q * 2 + c) ^ (t & 7)) << 4));
+                    codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
+                    codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
+                    codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
+                    codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
+                }
+                tmem_st16(tmem + q * 16, v);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        };
+        // this warp's rows are ready for the next MMAs
+        auto hand_over = [&]() {
+            tc_fence_before();
             __syncwarp();
+            if (ok && (t & 31) == 0) mbar_arrive(full + FWD_STAGES);
+        };
+        int byte = scale_of(0);
+        if (nt > 0) {
+            widen(0);
+            hand_over();
+        }
+        for (int it = 0; it < nt && ok; ++it) {
+            const float2 kk = dup2(row_factor(byte, down));
+            byte = scale_of(it + 1);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + FWD_STAGES + 1, (uint32_t)it & 1u, RO_POLLS));
             tc_fence_after();
+            if (!ok) break;
+            if (it + 1 < nt) widen(it + 1);                       // (the MMAs that read A are done)
             float d[64];
-            tmem_ld32(tmem + lanes + 64, *reinterpret_cast<float(*)[32]>(d));
-            tmem_ld32(tmem + lanes + 96, *reinterpret_cast<float(*)[32]>(d + 32));
+            tmem_ld32(tmem + 64, *reinterpret_cast<float(*)[32]>(d));
+            tmem_ld32(tmem + 96, *reinterpret_cast<float(*)[32]>(d + 32));
             tmem_ld_wait();
-            if (it + 1 < nt) {
-                widen(it + 1);
-                start(it + 1);
-            }
-            float2 e0 = make_float2(0.f, 0.f), e1 = e0;
-            const float2 kk = dup2(k);
+            if (it + 1 < nt) hand_over();
+            float2 e0 = make_float2(c2, 0.f), e1 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float4 c = cst[j];
                 const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
                 const float2 m = make_float2(-fabsf(p.x), -fabsf(p.y));
-                const float2 u = j % 4 != 3 ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
+                const float2 u = (j * FWD_FMA) % 8 < FWD_FMA ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
                 const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
                 e0 = fma2(make_float2(c.z, c.w), make_float2(lg2_mufu(y.x), lg2_mufu(y.y)), e0);
                 e1 = fma2(make_float2(c.z, c.w), make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)), e1);
             }
-            const int i = row0(it) + t;
-            const float e = ((e0.x + e0.y) + (e1.x + e1.y)) + c2;
+            const int i = first_row(g, it) + t;
+            const float e = (e0.x + e0.y) + (e1.x + e1.y);
             if (i < a.n) a.eps[i] = e;
             double s = i < a.n ? (double)e : 0.0;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if ((t & 31) == 0 && i < a.n) a.csum[i >> 5] = s;
         }
-        // a wait gave up: let this group's copies and MMAs in flight end (bounded) before the memory goes
-        if (!ok && t == 0) {
-            for (int st = 0; st < FWD_STAGES; ++st)
-                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(full + st, ph, 1u << 12);
-            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done, ph, 1u << 12);
-        }
     }
+    tc_fence_before();
     const int gave_up = __syncthreads_or(!ok);
     if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up ? 1u : 0u;
     if (warp == 0) {
