@@ -129,8 +129,10 @@ struct ReadoutArgs {
     float *dR1, *dc1, *dR2, *dc2;
     int ngroups;                         // groups of the gradient kernel that have tiles
     float* part;                         // [ngroups][64 h][128 f] their sums of D2
-    double* part2;                       // [CTAs] shares of dc2
-    double* colpart;                     // [ngroups][4 warps][128] column sums of g sigma, g ssp / ln2
+    int nseed;                           // CTAs of the seeds kernel
+    float* gat;                          // [n up to a multiple of 4] g of each atom
+    double* part2;                       // [nseed] shares of dc2
+    double* colpart;                     // [ngroups][4 warps][128] column sums of g sigma, g softplus / ln2
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
@@ -232,8 +234,8 @@ __device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
 // R1 as the MMA's B operand [64 h][128 f] (K-major core matrices), two fp16 terms of
 // R1 2^s with 2^s the power of two that brings the largest |R1| to [2^14, 2^15): hi + lo
 // carry 22 bits, and entries 2^-24 of the largest still lose nothing above 2^-39 of it.
-// Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the epilogues' exponentials
-// do not all keep a NaN).  All threads of the CTA; red: one word per warp.
+// Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the gradients' epilogue drops
+// a NaN of a single hidden unit).  All threads of the CTA; red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
 template <int THREADS>
 __device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, uint32_t* red)
@@ -280,22 +282,24 @@ __device__ __forceinline__ float row_factor(int byte, float down)
     return fminf(__uint_as_float((uint32_t)byte << 23) * down, 1e38f) * LOG2EF;
 }
 
-// Energies.  Four groups of 4 warps and one issuing warp share the CTA's R1.  A group takes
-// every (4 gridDim)-th tile of 128 atoms, one atom per thread: its row of codes is read from
-// the TMA stage, widened to fp16 (exact) and put into tensor memory as the MMA's A operand
-// (lane = atom), so D[atom][h] = codes . R1 comes back with a whole hidden layer per thread
-// and the sum over h needs no exchange.  A group widens tile it+1, reads D(it) into registers,
-// hands both on to the issuing warp and only then works on D(it), which hides the MMAs.
-// The issuing thread blocks while the tensor core's queue is full, so it does nothing else:
-// a group's own thread that issued held back its group.
-// Bound: the 2 transcendentals per hidden unit (all on the MUFU: 8 cycles an atom and SM)
-// and HBM (133 bytes: 5.9 cycles); FWD_FMA of 8 pairs' exponentials go to the FMA pipe.
-constexpr int FWD_GROUPS = 4, FWD_STAGES = 2, FWD_THREADS = FWD_GROUPS * 128 + 32;
-constexpr int FWD_FMA = 2;
+// Energies.  Three groups of 8 warps and one issuing warp share the CTA's R1.  A group takes
+// every (3 gridDim)-th tile of 128 atoms, a thread one atom and half of its hidden units:
+// half its row of codes is read from the TMA stage, widened to fp16 (exact) and put into
+// tensor memory as the MMA's A operand (lane = atom), so D[atom][h] = codes . R1 comes back
+// with 32 hidden units per thread; the halves meet through shared memory.  A group widens
+// tile it+1, reads D(it) into registers, hands both on to the issuing warp and only then
+// works on D(it), which hides the MMAs.  The issuing thread blocks while the tensor core's
+// queue is full, so it does nothing else.
+// Bound: 2 transcendentals per hidden unit on the MUFU, 8 cycles an atom and SM (HBM: 133
+// bytes, 5.9 cycles; MMAs: 4).  Exponentials on the FMA pipe (one pair in 8, 4, 2) cost more
+// issue slots than they free on the MUFU: 180, 186, 192 us against 180 for 4.2 M atoms.
+// One thread per atom with four groups of 4 warps (96 registers): 195 us.
+constexpr int FWD_GROUPS = 3, FWD_STAGES = 3, FWD_GT = 256, FWD_THREADS = FWD_GROUPS * FWD_GT + 32;
 constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
 constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
 constexpr uint32_t FWD_RED = FWD_CST + 32 * 16;
-constexpr uint32_t FWD_BAR = FWD_RED + 128;
+constexpr uint32_t FWD_EX = FWD_RED + 128;                       // per group: float[2][128], the upper halves' sums
+constexpr uint32_t FWD_BAR = FWD_EX + FWD_GROUPS * 2 * 128 * 4;
 constexpr int FWD_NBAR = FWD_STAGES + 2;                         // per group: stages full, A ready, MMAs done
 constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * FWD_NBAR + 16;
 
@@ -317,11 +321,11 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == FWD_GROUPS * 128) {                        // the first tiles are on their way before R1 is read
+    if (threadIdx.x == FWD_GROUPS * FWD_GT) {                        // the first tiles are on their way before R1 is read
         for (int g = 0; g < FWD_GROUPS; ++g) {
             uint64_t* full = bars + g * FWD_NBAR;
             for (int k = 0; k < FWD_STAGES; ++k) mbar_init(full + k, 1);
-            mbar_init(full + FWD_STAGES, 4);
+            mbar_init(full + FWD_STAGES, FWD_GT / 32);
             mbar_init(full + FWD_STAGES + 1, 1);
         }
         fence_mbar_init();
@@ -343,7 +347,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     tc_fence_after();
     bool ok = true;
 
-    if (warp == FWD_GROUPS * 4) {
+    if (warp == FWD_GROUPS * FWD_GT / 32) {
         // ---- issuing warp: every group's tiles in turn
         const uint32_t id = idesc_f16(128, HP, 0, 0);
         const uint64_t bhi = smem_desc(stages + FWD_R1, HP * 16, 128);
@@ -377,12 +381,14 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             for (int k = 0; k < FWD_GROUPS * FWD_NBAR; ++k)
                 for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(bars + k, ph, 1u << 12);
     } else {
-        const int g = threadIdx.x >> 7, t = threadIdx.x & 127;
+        const int g = threadIdx.x / FWD_GT, t = threadIdx.x & 127, half = (threadIdx.x >> 7) & 1;
+        float* ex = reinterpret_cast<float*>(sm + FWD_EX) + g * 256;
+        const int pair = 1 + g * 4 + (warp & 3);                  // named barrier of the two warps that share atoms
         uint64_t* full = bars + g * FWD_NBAR;
         const uint32_t tmem = *tslot + 128 * g + ((uint32_t)((warp & 3) * 32) << 16);    // A: 64 columns, D: 64 columns
         const uint32_t stage0 = stages + g * FWD_STAGES * TILE_BYTES + t * 128;
         const int nt = tiles_of(blockIdx.x + gridDim.x * g);
-        const float c2 = __ldg(a.c2);
+        const float c2 = half == 0 ? __ldg(a.c2) : 0.f;
         auto scale_of = [&](int it) {
             const int i = first_row(g, it) + t;
             return it < nt && i < a.n ? (int)__ldg(a.scales + i) : 127;
@@ -393,17 +399,17 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + st, (uint32_t)(it / FWD_STAGES) & 1u, RO_POLLS));
             const uint32_t src = stage0 + st * TILE_BYTES;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 uint32_t v[16];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint4 w = lds128(src + (((q * 2 + c) ^ (t & 7)) << 4));
+                    const uint4 w = lds128(src + (((half * 4 + q * 2 + c) ^ (t & 7)) << 4));
                     codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
                     codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
                     codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
                     codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
                 }
-                tmem_st16(tmem + q * 16, v);
+                tmem_st16(tmem + half * 32 + q * 16, v);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         };
@@ -423,31 +429,39 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             byte = scale_of(it + 1);
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + FWD_STAGES + 1, (uint32_t)it & 1u, RO_POLLS));
             tc_fence_after();
-            if (!ok) break;
+            if (!ok) {                                            // (the other warp must not wait for this one)
+                if (half == 1) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(pair) : "memory");
+                break;
+            }
             if (it + 1 < nt) widen(it + 1);                       // (the MMAs that read A are done)
-            float d[64];
-            tmem_ld32(tmem + 64, *reinterpret_cast<float(*)[32]>(d));
-            tmem_ld32(tmem + 96, *reinterpret_cast<float(*)[32]>(d + 32));
+            float d[32];
+            tmem_ld32(tmem + 64 + half * 32, d);
             tmem_ld_wait();
             if (it + 1 < nt) hand_over();
             float2 e0 = make_float2(c2, 0.f), e1 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float4 c = cst[j];
+            for (int j = 0; j < 16; ++j) {
+                const float4 c = cst[half * 16 + j];
                 const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
-                const float2 m = make_float2(-fabsf(p.x), -fabsf(p.y));
-                const float2 u = (j * FWD_FMA) % 8 < FWD_FMA ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
+                const float2 u = make_float2(ex2_mufu(-fabsf(p.x)), ex2_mufu(-fabsf(p.y)));
                 const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
                 e0 = fma2(make_float2(c.z, c.w), make_float2(lg2_mufu(y.x), lg2_mufu(y.y)), e0);
                 e1 = fma2(make_float2(c.z, c.w), make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)), e1);
             }
             const int i = first_row(g, it) + t;
-            const float e = (e0.x + e0.y) + (e1.x + e1.y);
-            if (i < a.n) a.eps[i] = e;
-            double s = i < a.n ? (double)e : 0.0;
+            float e = (e0.x + e0.y) + (e1.x + e1.y);
+            if (half == 1) {
+                ex[(it & 1) * 128 + t] = e;
+                asm volatile("barrier.cta.arrive %0, 64;" ::"r"(pair) : "memory");
+            } else {
+                asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair) : "memory");
+                e += ex[(it & 1) * 128 + t];
+                if (i < a.n) a.eps[i] = e;
+                double s = i < a.n ? (double)e : 0.0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((t & 31) == 0 && i < a.n) a.csum[i >> 5] = s;
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if ((t & 31) == 0 && i < a.n) a.csum[i >> 5] = s;
+            }
         }
     }
     tc_fence_before();
@@ -500,8 +514,11 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // Two groups of 8 warps share the CTA's R1; each takes a run of consecutive tiles.  A
 // thread holds one atom and half of its hidden units.  Per tile:
 //   GEMM1  D1[atom][h] = codes . R1 as in the energies;
-//   epilogue  per (atom, h): sigma(p), ssp(p); the column sums of g sigma and g ssp stay
-//     in registers, and sigma g_i scale_i goes to shared memory as an fp16 hi + residual pair;
+//   epilogue  per (atom, h), t = p log2(e) >= -126, y = 1 + 2^-t: sigma = 1 / y and
+//     ln(1 + e^p) = ln2 (t + log2 y), which for negative t keeps 2^-22 |t| absolutely (the
+//     same as the rounding of t); the column sums of g sigma and g (t + log2 y) stay in
+//     registers (ssp's -ln2 is dc2's share, taken off at the end), and sigma g_i scale_i
+//     goes to shared memory as an fp16 hi + residual pair;
 //   GEMM2  D2[f][h] += codes^T (sigma g scale): both operands are read MN-major, so the
 //     tile of codes widened once serves as it lies, and D2 stays in tensor memory from tile
 //     to tile.  R2 is a factor of whole columns and is applied at the very end.
@@ -518,10 +535,8 @@ constexpr uint32_t GRAD_GROUP = GRAD_B + 128 * 128 * 2;
 constexpr uint32_t GRAD_R1 = GRAD_GROUPS * GRAD_GROUP;
 constexpr uint32_t GRAD_CST = GRAD_R1 + 2 * R1_TERM;             // float[64]: c1 log2e
 constexpr uint32_t GRAD_RED = GRAD_CST + 64 * 4;
-constexpr uint32_t GRAD_ROW = GRAD_RED + 64;                     // per group: float2[128] (g, factor)
-constexpr uint32_t GRAD_MAX = GRAD_ROW + GRAD_GROUPS * 128 * 8;  // per group: uint32[4]
-constexpr uint32_t GRAD_SUM = GRAD_MAX + GRAD_GROUPS * 16;       // double[16]: the warps' parts of dc2
-constexpr uint32_t GRAD_BAR = GRAD_SUM + 16 * 8;
+constexpr uint32_t GRAD_MAX = GRAD_RED + 64;                     // per group: uint32[2][4]
+constexpr uint32_t GRAD_BAR = GRAD_MAX + GRAD_GROUPS * 32;
 constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * GRAD_GROUPS * (GRAD_STAGES + 2) + 16;
 static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
 constexpr int PART = HP * FP;                                    // one group's D2 sums, [h][f]
@@ -549,32 +564,48 @@ __device__ __forceinline__ float rcp_mufu(float x)
     return y;
 }
 
-// D[tmem] (+)= A[smem desc] B[smem desc], kind::f16
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate)
+// Seeds: gat[i] = g of atom i's replica (0 outside all replicas), and a CTA's share of
+// dc2 = sum_r g_r times the replica's atoms.  A thread takes 4 consecutive atoms: one
+// bisection for the first, steps from there (runs of empty replicas included).
+constexpr int SEED_ATOMS = 1024;         // atoms a CTA of 256 threads takes at a time
+constexpr int MAX_SEED = 1184;           // its CTAs
+__global__ void __launch_bounds__(256) k_readout_seeds(ReadoutArgs a)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// last r >= from with o_r <= i (o_from <= i), by doubling steps and bisection
-__device__ __forceinline__ int advance_replica(const ReadoutArgs& a, int from, int i)
-{
-    int lo = from, step = 1;
-    while (lo + step < a.R && off_at(a, lo + step) <= i) {
-        lo += step;
-        step *= 2;
+    pdl_trigger();
+    const int begin = off_at(a, 0), end = off_at(a, a.R);
+    for (long long c = (long long)blockIdx.x * SEED_ATOMS; c < a.n; c += (long long)gridDim.x * SEED_ATOMS) {
+        const int i0 = (int)c + threadIdx.x * 4;
+        if (i0 >= a.n) continue;
+        int lo = 0, hi = a.R;                                    // the last r with o_r <= i0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (off_at(a, mid) <= i0) lo = mid; else hi = mid;
+        }
+        int next = off_at(a, lo + 1);
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k;
+            while (next <= i && lo < a.R - 1) next = off_at(a, ++lo + 1);
+            v[k] = i >= begin && i < end ? __ldg(a.gE + lo) : 0.f;
+        }
+        *reinterpret_cast<float4*>(a.gat + i0) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    int hi = min(lo + step, a.R);                                // o_hi > i, or hi = R
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (off_at(a, mid) <= i) lo = mid; else hi = mid;
+    double s = 0.0;
+    for (int r = blockIdx.x * 256 + threadIdx.x; r < a.R; r += gridDim.x * 256) {
+        const int count = off_at(a, r + 1) - off_at(a, r);
+        const float g = __ldg(a.gE + r);
+        if (count > 0 && g != 0.f) s += (double)g * count;
     }
-    return lo;
+    __shared__ double ws[8];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < 8; ++w) s += ws[w];
+        a.part2[blockIdx.x] = s;
+    }
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
@@ -583,12 +614,11 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + GRAD_BAR);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + GRAD_GROUPS * (GRAD_STAGES + 2));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = threadIdx.x >> 8, t = threadIdx.x & 255, row = t & 127, half = t >> 7, wq = warp & 3;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int g = warp >> 3, t = threadIdx.x & 255, row = t & 127, half = t >> 7, wq = warp & 3;
     uint64_t* full = bars + g * (GRAD_STAGES + 2);
     uint64_t *done1 = full + GRAD_STAGES, *done2 = done1 + 1;
-    float2* rowv = reinterpret_cast<float2*>(sm + GRAD_ROW) + g * 128;
-    uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX) + g * 4;
+    uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX) + g * 8;
 
     pdl_trigger();
     if (warp == 0) {
@@ -608,28 +638,14 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     float* cst = reinterpret_cast<float*>(sm + GRAD_CST);
     if (threadIdx.x < HP) cst[threadIdx.x] = threadIdx.x < a.H ? __ldg(a.c1 + threadIdx.x) * LOG2EF : 0.f;
     const float down = stage_r1<GRAD_THREADS>(a, sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
-    // dc2: g_r times its atoms, over this CTA's share of the replicas
-    double seeds = 0.0;
-    for (int r = blockIdx.x * GRAD_THREADS + threadIdx.x; r < a.R; r += gridDim.x * GRAD_THREADS) {
-        const int count = off_at(a, r + 1) - off_at(a, r);
-        const float gr = __ldg(a.gE + r);
-        if (count > 0 && gr != 0.f) seeds += (double)gr * count;
-    }
-    for (int o = 16; o > 0; o >>= 1) seeds += __shfl_xor_sync(0xffffffffu, seeds, o);
-    double* wsum = reinterpret_cast<double*>(sm + GRAD_SUM);
-    if (lane == 0) wsum[warp] = seeds;
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0) {
-        seeds = 0.0;
-        for (int w = 0; w < GRAD_THREADS / 32; ++w) seeds += wsum[w];
-        a.part2[blockIdx.x] = seeds;
-    }
 
-    const uint32_t tmem = *tslot + 256 * g;                       // A: 64 columns, D1: 64, D2: 128
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0) + 256 * g;   // A: 64 columns, D1: 64, D2: 128
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t go = elect_one();
     const uint32_t xrow = base + GRAD_X + row * 16, brow = base + GRAD_B + row * 16;
     const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
     const uint64_t rhi = smem_desc(smem_u32(sm) + GRAD_R1, HP * 16, 128);
@@ -637,6 +653,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     const uint64_t xd = smem_desc(base + GRAD_X, 128, 2048), bd = smem_desc(base + GRAD_B, 128, 2048);
     float* part = a.part + (size_t)gid * PART;
     bool ok = true;
+    pdl_wait();                                                   // the seeds
 
     if (nt > 0) {
         float acc1[32], acc2[32];                                 // this thread's columns half * 32 + k
@@ -645,9 +662,66 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         for (int k = 0; k < 32; ++k) acc1[k] = acc2[k] = 0.f;
         int E = 120, held = 0, folded = 0;
         bool emptied = false;
-        int rep = -1;
-        const int end = off_at(a, a.R), begin = off_at(a, 0);
-
+        float seed;                                               // g and scale byte of this row, of the tile ahead
+        int byte;
+        auto fetch = [&](int it) {
+            const int i = row0(it) + row;
+            const bool in = it < nt && i < a.n;
+            seed = in ? a.gat[i] : 0.f;
+            byte = in ? (int)__ldg(a.scales + i) : 127;
+        };
+        // half a row of a tile's codes as fp16
+        auto codes = [&](int it, int q, uint32_t (&v)[16]) {
+            const uint32_t src = base + (it % GRAD_STAGES) * TILE_BYTES + row * 128;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint4 w = lds128(src + (((half * 4 + q * 2 + c) ^ (row & 7)) << 4));
+                codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
+                codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
+                codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
+                codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
+            }
+        };
+        // tile it's A into tensor memory (GEMM1 of the tile before has read it), and the
+        // largest finite |g scale| of its rows
+        auto widen = [&](int it) {
+            ok &= mbar_wait_bounded(full + it % GRAD_STAGES, (uint32_t)(it / GRAD_STAGES) & 1u, RO_POLLS);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t v[16];
+                codes(it, q, v);
+                tmem_st16(tmem + lanes + half * 32 + q * 16, v);
+            }
+            if (half == 0) {
+                uint32_t mb = __float_as_uint(seed * __uint_as_float((uint32_t)byte << 23)) & 0x7fffffffu;
+                if (mb >= 0x7f800000u) mb = 0;
+                mb = __reduce_max_sync(0xffffffffu, mb);
+                if (lane == 0) gmax[(it & 1) * 4 + wq] = mb;
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        };
+        // past the group's barrier: GEMM1 of tile it, and tile it + 1's codes into the stage
+        // that both widenings of tile it - 1 have read
+        auto gemm1 = [&](int it) {
+            tc_fence_before();
+            ok = group_and(1 + g, 256, ok);
+            if (ok && (warp & 7) == ((it + 4 * g) & 7)) {         // the warps take turns
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < FP / 16; ++ks)
+                    mma_ts(go, tmem + 64, tmem + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
+#pragma unroll
+                for (int ks = 0; ks < FP / 16; ++ks)
+                    mma_ts(go, tmem + 64, tmem + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
+                if (go) {
+                    mma_commit(done1);
+                    if (it > 0 && it + 1 < nt)
+                        tma_tile(base + (it + 1) % GRAD_STAGES * TILE_BYTES, &map, row0(it + 1), full + (it + 1) % GRAD_STAGES);
+                }
+            }
+            __syncwarp();
+        };
         // D2 2^-E into the group's sums (the MMAs that wrote it have completed)
         auto flush = [&]() {
             const float un = __uint_as_float((uint32_t)(127 - E) << 23);
@@ -675,137 +749,89 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             folded = 0;
         };
 
-        for (int it = 0; it < nt; ++it) {
-            const int st = it % GRAD_STAGES;
-            // ---- codes -> fp16 in tensor memory (GEMM1's A) and shared memory (GEMM2's A)
-            ok &= mbar_wait_bounded(full + st, (uint32_t)(it / GRAD_STAGES) & 1u, RO_POLLS);
-            __syncwarp();
-            uint32_t v[32];
-            const uint32_t src = base + st * TILE_BYTES + row * 128;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 q = lds128(src + (((half * 4 + c) ^ (row & 7)) << 4));
-                codes_to_half(q.x, v[c * 8 + 0], v[c * 8 + 1]);
-                codes_to_half(q.y, v[c * 8 + 2], v[c * 8 + 3]);
-                codes_to_half(q.z, v[c * 8 + 4], v[c * 8 + 5]);
-                codes_to_half(q.w, v[c * 8 + 6], v[c * 8 + 7]);
+        fetch(0);
+        widen(0);
+        gemm1(0);
+        for (int it = 0; it < nt && ok; ++it) {
+            // this row's seed, factor and scaled seed; a NaN scale (or weights) makes them NaN,
+            // a seed of 0 makes them 0 whatever the row holds
+            float gi = seed, k = 0.f, gx = 0.f;
+            if (gi != 0.f) {
+                k = row_factor(byte, down);
+                if (k != k) gi = k;
+                gx = gi * __uint_as_float((uint32_t)byte << 23);
             }
-            tmem_st32(tmem + lanes + half * 32, v);
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            if (it > 0) {                                         // GEMM2 of the last tile has read X and B
+            fetch(it + 1);
+            // ---- GEMM2 of the last tile is done: D2 may be emptied, X and B written
+            if (it > 0) {
                 ok &= mbar_wait_bounded(done2, (uint32_t)(it - 1) & 1u, RO_POLLS);
                 __syncwarp();
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xrow + (half * 8 + c) * 2048), "r"(v[c * 4]),
-                             "r"(v[c * 4 + 1]), "r"(v[c * 4 + 2]), "r"(v[c * 4 + 3])
-                             : "memory");
-            // ---- the row's gradient seed and factor (one half of the threads)
-            if (half == 0) {
-                const int i = row0(it) + row;
-                float gi = 0.f, k = 0.f, m = 0.f;
-                if (i >= begin && i < end) {
-                    rep = advance_replica(a, max(rep, 0), i);
-                    gi = __ldg(a.gE + rep);
-                    if (gi != 0.f) {
-                        const int byte = __ldg(a.scales + i);
-                        k = row_factor(byte, down);
-                        if (k != k) gi = k;                       // NaN scale (or weights): NaN from here on
-                        m = gi * __uint_as_float((uint32_t)byte << 23);
-                    }
-                }
-                rowv[row] = make_float2(gi, k);
-                // the scaled seed's magnitude, finite ones only
-                uint32_t mb = __float_as_uint(m) & 0x7fffffffu;
-                if (mb >= 0x7f800000u) mb = 0;
-                mb = __reduce_max_sync(0xffffffffu, mb);
-                if (lane == 0) gmax[wq] = mb;
-            }
-            tc_fence_before();
-            ok = group_and(1 + g, 256, ok);
-            if (!ok) break;
-            if (t == 0) {
                 tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)
-                    mma_f16_ts(tmem + 64, tmem + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
-#pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)
-                    mma_f16_ts(tmem + 64, tmem + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
-                mma_commit(done1);
-                if (it + GRAD_STAGES < nt) tma_tile(base + st * TILE_BYTES, &map, row0(it + GRAD_STAGES), full + st);
             }
-            __syncwarp();
-            const float2 rv = rowv[row];
-            const uint32_t mb = max(max(gmax[0], gmax[1]), max(gmax[2], gmax[3]));
-            if (mb >= 0x00800000u) {
-                const int e = max(-120, min(120, 13 - ((int)(mb >> 23) - 127)));
-                if (e < E) {
-                    tc_fence_after();
-                    if (held > 0) flush();
-                    E = e;
-                }
-            }
-            if (held >= GRAD_FLUSH) {
-                tc_fence_after();
-                flush();
-            }
+            const uint32_t* gm = gmax + (it & 1) * 4;
+            const uint32_t mb = max(max(gm[0], gm[1]), max(gm[2], gm[3]));
+            int e = E;
+            if (mb >= 0x00800000u) e = min(E, max(-120, min(120, 13 - ((int)(mb >> 23) - 127))));
+            if (held >= GRAD_FLUSH || (e < E && held > 0)) flush();
+            E = e;
             if (folded >= GRAD_FOLD) fold();
-            const float up = __uint_as_float((uint32_t)(127 + E) << 23);
-            const int i = row0(it) + row;
-            const float gx = rv.x != 0.f ? rv.x * __uint_as_float((uint32_t)__ldg(a.scales + i) << 23) * up : 0.f;
-            ok = mbar_wait_bounded(done1, (uint32_t)it & 1u, RO_POLLS);
-            __syncwarp();
-            tc_fence_after();
-            // ---- epilogue: 16 hidden units at a time
+            gx *= __uint_as_float((uint32_t)(127 + E) << 23);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float d[16];
-                tmem_ld16(tmem + lanes + 64 + half * 32 + q * 16, d);
-                tmem_ld_wait();
+                uint32_t v[16];
+                codes(it, q, v);
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {                     // 8 units: one 16-byte piece of each term
-                    uint32_t h[4], l[4];
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xrow + (half * 8 + q * 4 + c) * 2048),
+                                 "r"(v[c * 4]), "r"(v[c * 4 + 1]), "r"(v[c * 4 + 2]), "r"(v[c * 4 + 3])
+                                 : "memory");
+            }
+            // ---- tile it + 1 into tensor memory, D1 into registers, GEMM1 of tile it + 1
+            ok &= mbar_wait_bounded(done1, (uint32_t)it & 1u, RO_POLLS);
+            __syncwarp();
+            tc_fence_after();
+            if (it + 1 < nt) widen(it + 1);
+            float d[32];
+            tmem_ld32(tmem + lanes + 64 + half * 32, d);
+            tmem_ld_wait();
+            if (it + 1 < nt) gemm1(it + 1);
+            // ---- epilogue: 8 hidden units, one 16-byte piece of each term, at a time
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = q * 16 + o * 8 + 2 * j;
-                        const float2 b = *reinterpret_cast<const float2*>(cst + half * 32 + c);
-                        const float2 p = fma2(make_float2(d[o * 8 + 2 * j], d[o * 8 + 2 * j + 1]), dup2(rv.y), b);
-                        const float2 m = make_float2(-fabsf(p.x), -fabsf(p.y));
-                        const float2 u = j % 2 == 0 ? ex2_fma2(m) : make_float2(ex2_mufu(m.x), ex2_mufu(m.y));
-                        const float2 hu = mul2(dup2(0.5f), u), y = add2(hu, dup2(0.5f));
-                        const float2 ssp2 = add2(make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)),
-                                                 make_float2(lg2_mufu(y.x), lg2_mufu(y.y)));
-                        const float2 sg = mul2(make_float2(p.x >= 0.f ? 0.5f : hu.x, p.y >= 0.f ? 0.5f : hu.y),
-                                               make_float2(rcp_mufu(y.x), rcp_mufu(y.y)));
-                        const float2 a1 = fma2(dup2(rv.x), sg, make_float2(acc1[c], acc1[c + 1]));
-                        const float2 a2 = fma2(dup2(rv.x), ssp2, make_float2(acc2[c], acc2[c + 1]));
-                        acc1[c] = a1.x; acc1[c + 1] = a1.y;
-                        acc2[c] = a2.x; acc2[c + 1] = a2.y;
-                        const float2 w = mul2(dup2(gx), sg);
-                        split2_neg<0>(w.x, w.y, h[j], l[j]);
-                    }
-                    const uint32_t at = brow + (half * 4 + q * 2 + o) * 2048;
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                                 "r"(h[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 8 * 2048), "r"(l[0]), "r"(l[1]),
-                                 "r"(l[2]), "r"(l[3])
-                                 : "memory");
+            for (int q = 0; q < 4; ++q) {
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = q * 8 + 2 * j;
+                    const float2 b = *reinterpret_cast<const float2*>(cst + half * 32 + c);
+                    float2 p = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
+                    p = make_float2(fmaxf(p.x, -126.f), fmaxf(p.y, -126.f));
+                    const float2 y = add2(make_float2(ex2_mufu(-p.x), ex2_mufu(-p.y)), dup2(1.f));
+                    const float2 sg = make_float2(rcp_mufu(y.x), rcp_mufu(y.y));
+                    const float2 sp2 = add2(p, make_float2(lg2_mufu(y.x), lg2_mufu(y.y)));
+                    const float2 a1 = fma2(dup2(gi), sg, make_float2(acc1[c], acc1[c + 1]));
+                    const float2 a2 = fma2(dup2(gi), sp2, make_float2(acc2[c], acc2[c + 1]));
+                    acc1[c] = a1.x; acc1[c + 1] = a1.y;
+                    acc2[c] = a2.x; acc2[c + 1] = a2.y;
+                    const float2 w = mul2(dup2(gx), sg);
+                    split2_neg<0>(w.x, w.y, h[j], l[j]);
                 }
+                const uint32_t at = brow + (half * 4 + q) * 2048;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 8 * 2048), "r"(l[0]), "r"(l[1]),
+                             "r"(l[2]), "r"(l[3])
+                             : "memory");
             }
             fence_proxy_async_smem();
             tc_fence_before();
             ok = group_and(1 + g, 256, ok);
-            if (!ok) break;
-            if (t == 0) {
+            if (ok && (warp & 7) == ((it + 4 * g + 2) & 7)) {
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)                    // 16 atoms a step
-                    mma_f16_ss(tmem + 128, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
-                               held > 0 || ks > 0 ? 1u : 0u);
-                mma_commit(done2);
+                    mma_ss(go, tmem + 128, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
+                           held > 0 || ks > 0 ? 1u : 0u);
+                if (go) mma_commit(done2);
             }
             __syncwarp();
             ++held;
@@ -839,8 +865,8 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     }
 }
 
-// dR1 = R2_h sum of the groups' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 sum of g ssp / ln2,
-// dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
+// dR1 = R2_h sum of the groups' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 (sum of
+// g softplus / ln2 - sum of g), dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
 // columns (CTAs 0 .. 4 H - 1: R1, a quarter of the f of one h each; then 4 for c1 and R2;
 // then c2), its 8 warps a share of the partial sums each.
 __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
@@ -861,8 +887,10 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
         const double* p = a.colpart + (b - nb) * 32 + lane;
 #pragma unroll 8
         for (int k = w; k < a.ngroups * 4; k += 8) s += p[(size_t)k * 128];
+        if (b >= nb + 2)
+            for (int k = w; k < a.nseed; k += 8) s -= a.part2[k];  // ssp = softplus - ln2
     } else {
-        for (int k = threadIdx.x; k < a.ncta; k += 256) s += a.part2[k];
+        for (int k = threadIdx.x; k < a.nseed; k += 256) s += a.part2[k];
     }
     red[w][lane] = s;
     __syncthreads();
@@ -971,8 +999,9 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
     if (!bytes || n_atoms < 0) return SCHNET_ERR_INVALID_ARG;
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
     const size_t tiles = ((size_t)n_atoms + 127) / 128, groups = std::min<size_t>(tiles, GRAD_GROUPS * MAX_SM);
-    *bytes = (sizeof(uint32_t) + sizeof(double)) * MAX_SM + std::max(sizeof(double) * 4 * tiles,
-                                                  groups * (sizeof(float) * PART + sizeof(double) * 4 * 128));
+    *bytes = sizeof(uint32_t) * MAX_SM +
+             std::max(sizeof(double) * 4 * tiles, sizeof(double) * MAX_SEED + groups * (sizeof(float) * PART + sizeof(double) * 4 * 128) +
+                                                      sizeof(float) * 128 * tiles);
     return SCHNET_OK;
 }
 
@@ -1027,15 +1056,18 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     a.ngroups = std::min(ntiles, GRAD_GROUPS * nsm);
     a.ncta = std::min(ntiles, nsm);
     a.status = (uint32_t*)d_workspace;
+    a.nseed = a.n > 0 ? std::min(std::max((a.n + SEED_ATOMS - 1) / SEED_ATOMS, (a.R + 1023) / 1024), MAX_SEED) : 0;
     a.part2 = (double*)(a.status + MAX_SM);
-    a.colpart = a.part2 + MAX_SM;
+    a.colpart = a.part2 + MAX_SEED;
     a.part = (float*)(a.colpart + (size_t)a.ngroups * 4 * 128);
+    a.gat = a.part + (size_t)a.ngroups * PART;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
         CUtensorMap map;
         if (!code_map(a, &map) || !allow_smem((const void*)k_readout_grad, GRAD_SMEM, g_grad_set))
             return SCHNET_ERR_CUDA;
-        k_readout_grad<<<a.ncta, GRAD_THREADS, GRAD_SMEM, s>>>(map, a);
+        k_readout_seeds<<<a.nseed, 256, 0, s>>>(a);
+        if (launch_pdl(k_readout_grad, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a) != cudaSuccess) return SCHNET_ERR_CUDA;
     }
     if (launch_pdl(k_readout_grad_sum, 4 * a.H + 5, 256, 0, s, a) != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
