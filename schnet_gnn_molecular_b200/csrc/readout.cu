@@ -127,12 +127,11 @@ struct ReadoutArgs {
     int ncta;
     const float* gE;
     float *dR1, *dc1, *dR2, *dc2;
-    int ngroups;                         // groups of the gradient kernel that have tiles
-    float* part;                         // [ngroups][64 h][128 f] their sums of D2
+    float* part;                         // [CTAs][64 h][128 f] sums of D2
     int nseed;                           // CTAs of the seeds kernel
     float* gat;                          // [n up to a multiple of 4] g of each atom
     double* part2;                       // [nseed] shares of dc2
-    double* colpart;                     // [ngroups][4 warps][128] column sums of g sigma, g softplus / ln2
+    double* colpart;                     // [CTAs][4 warps][128] column sums of g sigma, g softplus / ln2
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
@@ -511,8 +510,10 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // ---------------------------------------------------------------------------
 // readout weight gradients
 // ---------------------------------------------------------------------------
-// Two groups of 8 warps share the CTA's R1; each takes a run of consecutive tiles.  A
-// thread holds one atom and half of its hidden units.  Per tile:
+// A CTA takes a run of consecutive tiles.  Four widening warps turn codes into fp16, into
+// tensor memory (GEMM1's A) and shared memory (GEMM2's A), and put down each row's seed
+// and scale; the first of them also starts copies and MMAs.  Sixteen epilogue warps hold
+// one atom and 16 hidden units a thread.  Per tile:
 //   GEMM1  D1[atom][h] = codes . R1 as in the energies;
 //   epilogue  per (atom, h), t = p log2(e) >= -126, y = 1 + 2^-t: sigma = 1 / y and
 //     ln(1 + e^p) = ln2 (t + log2 y), which for negative t keeps 2^-22 |t| absolutely (the
@@ -522,31 +523,37 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 //   GEMM2  D2[f][h] += codes^T (sigma g scale): both operands are read MN-major, so the
 //     tile of codes widened once serves as it lies, and D2 stays in tensor memory from tile
 //     to tile.  R2 is a factor of whole columns and is applied at the very end.
+// A and D1 are doubled, X (the codes in shared memory) is held three times and B (the
+// pairs) twice: every wait is for something handed over a tile earlier.
 // The pair's power-of-two scale 2^E brings the largest |g_i scale_i| seen so far to
 // [2^13, 2^14); when a tile has a larger one, D2 is emptied first and E lowered.  The
 // tensor core's fp32 accumulation does not round to nearest, so D2 is emptied into fp32
 // sums in global memory every GRAD_FLUSH tiles in any case, and the column sums are folded
 // into float64 every GRAD_FOLD tiles.
-constexpr int GRAD_GROUPS = 2, GRAD_STAGES = 2, GRAD_THREADS = GRAD_GROUPS * 256;
+// Bound: 3 transcendentals per hidden unit on the MUFU, 12 cycles an atom and SM (MMAs: 8,
+// shared memory: 10, HBM: 5.8).
+constexpr int GRAD_EPI = 512, GRAD_THREADS = GRAD_EPI + 128, GRAD_XS = 3;
 constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
-constexpr uint32_t GRAD_X = GRAD_STAGES * TILE_BYTES;            // within a group: codes as fp16 [128][128]
-constexpr uint32_t GRAD_B = GRAD_X + 128 * 128 * 2;              // [128][64 hi | 64 residual]
-constexpr uint32_t GRAD_GROUP = GRAD_B + 128 * 128 * 2;
-constexpr uint32_t GRAD_R1 = GRAD_GROUPS * GRAD_GROUP;
+constexpr uint32_t GRAD_OP = 128 * 128 * 2;                      // codes as fp16 [128][128], or [128][64 hi | 64 residual]
+constexpr uint32_t GRAD_X = 2 * TILE_BYTES;
+constexpr uint32_t GRAD_B = GRAD_X + GRAD_XS * GRAD_OP;
+constexpr uint32_t GRAD_R1 = GRAD_B + 2 * GRAD_OP;
 constexpr uint32_t GRAD_CST = GRAD_R1 + 2 * R1_TERM;             // float[64]: c1 log2e
 constexpr uint32_t GRAD_RED = GRAD_CST + 64 * 4;
-constexpr uint32_t GRAD_MAX = GRAD_RED + 64;                     // per group: uint32[2][4]
-constexpr uint32_t GRAD_BAR = GRAD_MAX + GRAD_GROUPS * 32;
-constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * GRAD_GROUPS * (GRAD_STAGES + 2) + 16;
+constexpr uint32_t GRAD_SEED = GRAD_RED + 128;                   // float[GRAD_XS][128]: the rows' seeds
+constexpr uint32_t GRAD_BYTE = GRAD_SEED + GRAD_XS * 128 * 4;    // uint8[GRAD_XS][128]: their scales
+constexpr uint32_t GRAD_MAX = GRAD_BYTE + GRAD_XS * 128;         // uint32[GRAD_XS][4]: largest finite |g scale| of a warp
+constexpr uint32_t GRAD_BAR = GRAD_MAX + GRAD_XS * 16;
+constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * 10 + 16;
 static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
 constexpr int PART = HP * FP;                                    // one group's D2 sums, [h][f]
 
-// sums of v[0..31] over the warp's lanes: lane c gets column c's
-__device__ __forceinline__ float fold_columns(float (&v)[32])
+// sums of v[0..15] over the warp's lanes: lanes c and c + 16 get column c's
+__device__ __forceinline__ float fold_columns(float (&v)[16])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
+    for (int s = 8; s > 0; s >>= 1) {
         const bool up = lane & s;
 #pragma unroll
         for (int k = 0; k < s; ++k) {
@@ -554,7 +561,7 @@ __device__ __forceinline__ float fold_columns(float (&v)[32])
             v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 __device__ __forceinline__ float rcp_mufu(float x)
@@ -612,28 +619,37 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
+    // each twice, by the tile's parity
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + GRAD_BAR);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + GRAD_GROUPS * (GRAD_STAGES + 2));
+    uint64_t *full = bars, *ready1 = bars + 2, *done1 = bars + 4, *ready2 = bars + 6, *done2 = bars + 8;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 10);
+    float* seeds = reinterpret_cast<float*>(sm + GRAD_SEED);
+    uint8_t* bytes = sm + GRAD_BYTE;
+    uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int g = warp >> 3, t = threadIdx.x & 255, row = t & 127, half = t >> 7, wq = warp & 3;
-    uint64_t* full = bars + g * (GRAD_STAGES + 2);
-    uint64_t *done1 = full + GRAD_STAGES, *done2 = done1 + 1;
-    uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX) + g * 8;
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const int ntiles = (a.n + 127) / 128;
+    const int first = (int)((long long)ntiles * blockIdx.x / a.ncta);
+    const int nt = (int)((long long)ntiles * (blockIdx.x + 1) / a.ncta) - first;
+    const uint32_t base = smem_u32(sm);
+    auto row0 = [&](int it) { return (first + it) * 128; };
+    auto fetch_tile = [&](int it) { tma_tile(base + (it & 1) * TILE_BYTES, &map, row0(it), full + (it & 1)); };
 
     pdl_trigger();
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    const uint32_t base = smem_u32(sm) + g * GRAD_GROUP;
-    const int ntiles = (a.n + 127) / 128, gid = blockIdx.x + gridDim.x * g;
-    const int first = gid < a.ngroups ? (int)((long long)ntiles * gid / a.ngroups) : 0;
-    const int nt = gid < a.ngroups ? (int)((long long)ntiles * (gid + 1) / a.ngroups) - first : 0;
-    auto row0 = [&](int it) { return (first + it) * 128; };
-    if (t == 0) {                                                 // the first tiles are on their way before R1 is read
-        for (int k = 0; k < GRAD_STAGES + 2; ++k) mbar_init(full + k, 1);
+    if (threadIdx.x == GRAD_EPI) {                                // the first tiles are on their way before R1 is read
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(full + k, 1);
+            mbar_init(ready1 + k, 4);
+            mbar_init(done1 + k, 1);
+            mbar_init(ready2 + k, GRAD_EPI / 32);
+            mbar_init(done2 + k, 1);
+        }
         fence_mbar_init();
-        for (int it = 0; it < GRAD_STAGES && it < nt; ++it) tma_tile(base + it * TILE_BYTES, &map, row0(it), full + it);
+        for (int it = 0; it < 2 && it < nt; ++it) fetch_tile(it);
     }
     float* cst = reinterpret_cast<float*>(sm + GRAD_CST);
     if (threadIdx.x < HP) cst[threadIdx.x] = threadIdx.x < a.H ? __ldg(a.c1 + threadIdx.x) * LOG2EF : 0.f;
@@ -643,100 +659,148 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     __syncthreads();
     tc_fence_after();
 
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0) + 256 * g;   // A: 64 columns, D1: 64, D2: 128
-    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t go = elect_one();
-    const uint32_t xrow = base + GRAD_X + row * 16, brow = base + GRAD_B + row * 16;
-    const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
-    const uint64_t rhi = smem_desc(smem_u32(sm) + GRAD_R1, HP * 16, 128);
-    const uint64_t rlo = smem_desc(smem_u32(sm) + GRAD_R1 + R1_TERM, HP * 16, 128);
-    const uint64_t xd = smem_desc(base + GRAD_X, 128, 2048), bd = smem_desc(base + GRAD_B, 128, 2048);
-    float* part = a.part + (size_t)gid * PART;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);    // D2: 128 columns, A: 2 x 64, D1: 2 x 64
+    const uint32_t tm = tmem + ((uint32_t)(wq * 32) << 16);
     bool ok = true;
-    pdl_wait();                                                   // the seeds
+    int E = 120, held = 0;
+    // the scale of a tile, and whether D2 has to be emptied before it is added; x = tile % GRAD_XS
+    auto plan = [&](uint32_t x, int& e) {
+        const uint32_t* gm = gmax + x * 4;
+        const uint32_t mb = max(max(gm[0], gm[1]), max(gm[2], gm[3]));
+        e = E;
+        if (mb >= 0x00800000u) e = min(E, max(-120, min(120, 13 - ((int)(mb >> 23) - 127))));
+        return held >= GRAD_FLUSH || (e < E && held > 0);
+    };
+    // tile `it`'s phase of one of the doubled barriers
+    auto wait = [&](uint64_t* two, int it) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(two + (it & 1), (uint32_t)(it >> 1) & 1u, RO_POLLS));
+        return ok;
+    };
+    auto next = [](uint32_t x) { return x == GRAD_XS - 1 ? 0u : x + 1; };
 
-    if (nt > 0) {
-        float acc1[32], acc2[32];                                 // this thread's columns half * 32 + k
-        double sum1 = 0.0, sum2 = 0.0;                            // this lane's column, folded
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc1[k] = acc2[k] = 0.f;
-        int E = 120, held = 0, folded = 0;
-        bool emptied = false;
-        float seed;                                               // g and scale byte of this row, of the tile ahead
+    if (warp >= GRAD_EPI / 32) {
+        // ---- widening warps, one row of codes a thread; the first one starts copies and MMAs
+        const bool leader = warp == GRAD_EPI / 32;
+        const uint32_t go = elect_one();
+        const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
+        const uint64_t rhi = smem_desc(base + GRAD_R1, HP * 16, 128);
+        const uint64_t rlo = smem_desc(base + GRAD_R1 + R1_TERM, HP * 16, 128);
+        float seed;
         int byte;
-        auto fetch = [&](int it) {
+        auto load = [&](int it) {
             const int i = row0(it) + row;
             const bool in = it < nt && i < a.n;
             seed = in ? a.gat[i] : 0.f;
             byte = in ? (int)__ldg(a.scales + i) : 127;
         };
-        // half a row of a tile's codes as fp16
-        auto codes = [&](int it, int q, uint32_t (&v)[16]) {
-            const uint32_t src = base + (it % GRAD_STAGES) * TILE_BYTES + row * 128;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint4 w = lds128(src + (((half * 4 + q * 2 + c) ^ (row & 7)) << 4));
-                codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
-                codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
-                codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
-                codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
-            }
-        };
-        // tile it's A into tensor memory (GEMM1 of the tile before has read it), and the
-        // largest finite |g scale| of its rows
-        auto widen = [&](int it) {
-            ok &= mbar_wait_bounded(full + it % GRAD_STAGES, (uint32_t)(it / GRAD_STAGES) & 1u, RO_POLLS);
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v[16];
-                codes(it, q, v);
-                tmem_st16(tmem + lanes + half * 32 + q * 16, v);
-            }
-            if (half == 0) {
-                uint32_t mb = __float_as_uint(seed * __uint_as_float((uint32_t)byte << 23)) & 0x7fffffffu;
-                if (mb >= 0x7f800000u) mb = 0;
-                mb = __reduce_max_sync(0xffffffffu, mb);
-                if (lane == 0) gmax[(it & 1) * 4 + wq] = mb;
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        };
-        // past the group's barrier: GEMM1 of tile it, and tile it + 1's codes into the stage
-        // that both widenings of tile it - 1 have read
         auto gemm1 = [&](int it) {
-            tc_fence_before();
-            ok = group_and(1 + g, 256, ok);
-            if (ok && (warp & 7) == ((it + 4 * g) & 7)) {         // the warps take turns
-                tc_fence_after();
+            const uint32_t A = tmem + 128 + (it & 1) * 64, D = tmem + 256 + (it & 1) * 64;
 #pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)
-                    mma_ts(go, tmem + 64, tmem + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < FP / 16; ++ks)                  // the small terms first
+                mma_ts(go, D, A + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
 #pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)
-                    mma_ts(go, tmem + 64, tmem + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
-                if (go) {
-                    mma_commit(done1);
-                    if (it > 0 && it + 1 < nt)
-                        tma_tile(base + (it + 1) % GRAD_STAGES * TILE_BYTES, &map, row0(it + 1), full + (it + 1) % GRAD_STAGES);
-                }
-            }
-            __syncwarp();
+            for (int ks = 0; ks < FP / 16; ++ks)
+                mma_ts(go, D, A + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
+            if (go) mma_commit(done1 + (it & 1));
         };
-        // D2 2^-E into the group's sums (the MMAs that wrote it have completed)
+        uint32_t x = 0, xb = 0;                                   // it % GRAD_XS, and the next GEMM2's
+        auto gemm2 = [&](int it) {
+            int e;
+            if (plan(xb, e)) held = 0;
+            E = e;
+            const uint64_t xd = smem_desc(base + GRAD_X + xb * GRAD_OP, 128, 2048);
+            const uint64_t bd = smem_desc(base + GRAD_B + (it & 1) * GRAD_OP, 128, 2048);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)                        // 16 atoms a step
+                mma_ss(go, tmem, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
+                       held > 0 || ks > 0 ? 1u : 0u);
+            if (go) mma_commit(done2 + (it & 1));
+            ++held;
+            xb = next(xb);
+        };
+        pdl_wait();                                               // the seeds
+        load(0);
+        for (int it = 0; it < nt; ++it) {
+            if (!wait(full, it)) break;
+            if (it >= 2 && !wait(done1, it - 2)) break;           // A is free
+            if (it >= GRAD_XS && !wait(done2, it - GRAD_XS)) break;    // X and the rows' slots are free
+            const uint32_t src = base + (it & 1) * TILE_BYTES + row * 128;
+            const uint32_t to = base + GRAD_X + x * GRAD_OP + row * 16;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v[16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 w = lds128(src + (((q * 2 + c) ^ (row & 7)) << 4));
+                    codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
+                    codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
+                    codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
+                    codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
+                }
+                tmem_st16(tm + 128 + (it & 1) * 64 + q * 16, v);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (q * 4 + c) * 2048), "r"(v[c * 4]),
+                                 "r"(v[c * 4 + 1]), "r"(v[c * 4 + 2]), "r"(v[c * 4 + 3])
+                                 : "memory");
+            }
+            seeds[x * 128 + row] = seed;
+            bytes[x * 128 + row] = (uint8_t)byte;
+            uint32_t mb = __float_as_uint(seed * __uint_as_float((uint32_t)byte << 23)) & 0x7fffffffu;
+            mb = __reduce_max_sync(0xffffffffu, mb >= 0x7f800000u ? 0u : mb);
+            if (lane == 0) gmax[x * 4 + wq] = mb;
+            load(it + 1);
+            fence_proxy_async_smem();
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready1 + (it & 1));
+            x = next(x);
+            if (leader) {
+                if (!wait(ready1, it)) break;
+                if (go && it + 2 < nt) fetch_tile(it + 2);        // every row of the stage has been read
+                if (it >= 2 && !wait(ready2, it - 2)) break;      // D1 has been read, B written
+                tc_fence_after();
+                gemm1(it);
+                if (it >= 2) gemm2(it - 2);
+                __syncwarp();
+            }
+        }
+        if (leader) {
+            for (int it = max(nt - 2, 0); it < nt && ok; ++it) {
+                if (!wait(ready2, it)) break;
+                tc_fence_after();
+                gemm2(it);
+                __syncwarp();
+            }
+            if (!ok && go)   // a wait gave up: let the copies and MMAs in flight end (bounded) before the memory goes
+                for (int k = 0; k < 10; ++k)
+                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(bars + k, ph, 1u << 12);
+        }
+    } else {
+        // ---- epilogue warps
+        const int part = warp >> 2;
+        float* sums = a.part + (size_t)blockIdx.x * PART;
+        float acc1[16], acc2[16];                                 // this thread's columns part * 16 + k
+        double sum1 = 0.0, sum2 = 0.0;                            // column part * 16 + lane % 16, folded
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc1[k] = acc2[k] = 0.f;
+        int folded = 0;
+        bool emptied = false;
+        // D2 2^-E into the CTA's sums (the MMAs that wrote it have completed); an address
+        // belongs to one thread, so the order of its additions is fixed
         auto flush = [&]() {
             const float un = __uint_as_float((uint32_t)(127 - E) << 23);
+            float hi[16], lo[16];
+            tmem_ld16(tm + part * 16, hi);
+            tmem_ld16(tm + 64 + part * 16, lo);
+            tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float hi[16], lo[16];
-                tmem_ld16(tmem + lanes + 128 + half * 32 + q * 16, hi);
-                tmem_ld16(tmem + lanes + 192 + half * 32 + q * 16, lo);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float* o = part + (half * 32 + q * 16 + k) * FP + wq * 32 + lane;
-                    const float v = (hi[k] - lo[k]) * un;         // the residual is stored negated
-                    *o = emptied ? *o + v : v;
-                }
+            for (int k = 0; k < 16; ++k) {
+                float* o = sums + (part * 16 + k) * FP + row;
+                const float v = (hi[k] - lo[k]) * un;             // the residual is stored negated
+                if (emptied) atomicAdd(o, v);
+                else *o = v;
             }
             emptied = true;
             held = 0;
@@ -745,64 +809,44 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             sum1 += (double)fold_columns(acc1);
             sum2 += (double)fold_columns(acc2);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) acc1[k] = acc2[k] = 0.f;
+            for (int k = 0; k < 16; ++k) acc1[k] = acc2[k] = 0.f;
             folded = 0;
         };
-
-        fetch(0);
-        widen(0);
-        gemm1(0);
-        for (int it = 0; it < nt && ok; ++it) {
-            // this row's seed, factor and scaled seed; a NaN scale (or weights) makes them NaN,
-            // a seed of 0 makes them 0 whatever the row holds
-            float gi = seed, k = 0.f, gx = 0.f;
-            if (gi != 0.f) {
-                k = row_factor(byte, down);
-                if (k != k) gi = k;
-                gx = gi * __uint_as_float((uint32_t)byte << 23);
-            }
-            fetch(it + 1);
-            // ---- GEMM2 of the last tile is done: D2 may be emptied, X and B written
-            if (it > 0) {
-                ok &= mbar_wait_bounded(done2, (uint32_t)(it - 1) & 1u, RO_POLLS);
-                __syncwarp();
+        uint32_t x = 0;                                           // it % GRAD_XS
+        for (int it = 0; it < nt; ++it) {
+            if (!wait(done1, it)) break;
+            tc_fence_after();
+            int e;
+            if (plan(x, e)) {
+                if (!wait(done2, it - 1)) break;
                 tc_fence_after();
+                flush();
             }
-            const uint32_t* gm = gmax + (it & 1) * 4;
-            const uint32_t mb = max(max(gm[0], gm[1]), max(gm[2], gm[3]));
-            int e = E;
-            if (mb >= 0x00800000u) e = min(E, max(-120, min(120, 13 - ((int)(mb >> 23) - 127))));
-            if (held >= GRAD_FLUSH || (e < E && held > 0)) flush();
             E = e;
             if (folded >= GRAD_FOLD) fold();
-            gx *= __uint_as_float((uint32_t)(127 + E) << 23);
+            float d[16];
+            tmem_ld16(tm + 256 + (it & 1) * 64 + part * 16, d);
+            // the row's seed, factor and scaled seed; a NaN scale (or weights) makes them NaN,
+            // a seed of 0 makes them 0 whatever the row holds
+            float gi = seeds[x * 128 + row], k = 0.f, gx = 0.f;
+            if (gi != 0.f) {
+                const int byte = bytes[x * 128 + row];
+                k = row_factor(byte, down);
+                if (k != k) gi = k;
+                gx = gi * __uint_as_float((uint32_t)byte << 23) * __uint_as_float((uint32_t)(127 + E) << 23);
+            }
+            x = next(x);
+            if (it >= 2 && !wait(done2, it - 2)) break;           // B is free
+            tmem_ld_wait();
+            // 8 hidden units, one 16-byte piece of each term, at a time
+            const uint32_t to = base + GRAD_B + (it & 1) * GRAD_OP + part * 2 * 2048 + row * 16;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                uint32_t v[16];
-                codes(it, q, v);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(xrow + (half * 8 + q * 4 + c) * 2048),
-                                 "r"(v[c * 4]), "r"(v[c * 4 + 1]), "r"(v[c * 4 + 2]), "r"(v[c * 4 + 3])
-                                 : "memory");
-            }
-            // ---- tile it + 1 into tensor memory, D1 into registers, GEMM1 of tile it + 1
-            ok &= mbar_wait_bounded(done1, (uint32_t)it & 1u, RO_POLLS);
-            __syncwarp();
-            tc_fence_after();
-            if (it + 1 < nt) widen(it + 1);
-            float d[32];
-            tmem_ld32(tmem + lanes + 64 + half * 32, d);
-            tmem_ld_wait();
-            if (it + 1 < nt) gemm1(it + 1);
-            // ---- epilogue: 8 hidden units, one 16-byte piece of each term, at a time
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = q * 8 + 2 * j;
-                    const float2 b = *reinterpret_cast<const float2*>(cst + half * 32 + c);
+                    const float2 b = *reinterpret_cast<const float2*>(cst + part * 16 + c);
                     float2 p = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
                     p = make_float2(fmaxf(p.x, -126.f), fmaxf(p.y, -126.f));
                     const float2 y = add2(make_float2(ex2_mufu(-p.x), ex2_mufu(-p.y)), dup2(1.f));
@@ -815,44 +859,28 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                     const float2 w = mul2(dup2(gx), sg);
                     split2_neg<0>(w.x, w.y, h[j], l[j]);
                 }
-                const uint32_t at = brow + (half * 4 + q) * 2048;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + q * 2048), "r"(h[0]), "r"(h[1]),
+                             "r"(h[2]), "r"(h[3])
                              : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + 8 * 2048), "r"(l[0]), "r"(l[1]),
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (8 + q) * 2048), "r"(l[0]), "r"(l[1]),
                              "r"(l[2]), "r"(l[3])
                              : "memory");
             }
             fence_proxy_async_smem();
             tc_fence_before();
-            ok = group_and(1 + g, 256, ok);
-            if (ok && (warp & 7) == ((it + 4 * g + 2) & 7)) {
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)                    // 16 atoms a step
-                    mma_ss(go, tmem + 128, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
-                           held > 0 || ks > 0 ? 1u : 0u);
-                if (go) mma_commit(done2);
-            }
             __syncwarp();
+            if (lane == 0) mbar_arrive(ready2 + (it & 1));
             ++held;
             ++folded;
         }
-        if (ok) ok = mbar_wait_bounded(done2, (uint32_t)(nt - 1) & 1u, RO_POLLS);
-        __syncwarp();
-        if (group_and(1 + g, 256, ok)) {
+        if (ok && nt > 0 && wait(done2, nt - 1)) {
             tc_fence_after();
             flush();
             fold();
-            double* o = a.colpart + ((size_t)gid * 4 + wq) * 128 + half * 32 + lane;
-            o[0] = sum1;
-            o[64] = sum2;
-        } else {
-            ok = false;
-            if (t == 0) {      // let this group's copies and MMAs in flight end (bounded) before the memory goes
-                for (int st = 0; st < GRAD_STAGES; ++st)
-                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(full + st, ph, 1u << 12);
-                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done1, ph, 1u << 12);
-                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(done2, ph, 1u << 12);
+            if (lane < 16) {
+                double* o = a.colpart + ((size_t)blockIdx.x * 4 + wq) * 128 + part * 16 + lane;
+                o[0] = sum1;
+                o[64] = sum2;
             }
         }
     }
@@ -861,11 +889,11 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up ? 1u : 0u;
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(*tslot, 512);
+        tmem_dealloc(tmem, 512);
     }
 }
 
-// dR1 = R2_h sum of the groups' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 (sum of
+// dR1 = R2_h sum of the CTAs' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 (sum of
 // g softplus / ln2 - sum of g), dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
 // columns (CTAs 0 .. 4 H - 1: R1, a quarter of the f of one h each; then 4 for c1 and R2;
 // then c2), its 8 warps a share of the partial sums each.
@@ -882,11 +910,11 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     if (b < nb) {
         const float* p = a.part + (b >> 2) * FP + (b & 3) * 32 + lane;
 #pragma unroll 8
-        for (int k = w; k < a.ngroups; k += 8) s += (double)p[(size_t)k * PART];
+        for (int k = w; k < a.ncta; k += 8) s += (double)p[(size_t)k * PART];
     } else if (b < nb + 4) {
         const double* p = a.colpart + (b - nb) * 32 + lane;
 #pragma unroll 8
-        for (int k = w; k < a.ngroups * 4; k += 8) s += p[(size_t)k * 128];
+        for (int k = w; k < a.ncta * 4; k += 8) s += p[(size_t)k * 128];
         if (b >= nb + 2)
             for (int k = w; k < a.nseed; k += 8) s -= a.part2[k];  // ssp = softplus - ln2
     } else {
@@ -998,9 +1026,9 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
 {
     if (!bytes || n_atoms < 0) return SCHNET_ERR_INVALID_ARG;
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
-    const size_t tiles = ((size_t)n_atoms + 127) / 128, groups = std::min<size_t>(tiles, GRAD_GROUPS * MAX_SM);
+    const size_t tiles = ((size_t)n_atoms + 127) / 128, ctas = std::min<size_t>(tiles, MAX_SM);
     *bytes = sizeof(uint32_t) * MAX_SM +
-             std::max(sizeof(double) * 4 * tiles, sizeof(double) * MAX_SEED + groups * (sizeof(float) * PART + sizeof(double) * 4 * 128) +
+             std::max(sizeof(double) * 4 * tiles, sizeof(double) * MAX_SEED + ctas * (sizeof(float) * PART + sizeof(double) * 4 * 128) +
                                                       sizeof(float) * 128 * tiles);
     return SCHNET_OK;
 }
@@ -1052,15 +1080,13 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     if (cudaPeekAtLastError() != cudaSuccess) return SCHNET_ERR_CUDA;
     a.gE = d_grad_energy;
     a.dR1 = d_dR1; a.dc1 = d_dc1; a.dR2 = d_dR2; a.dc2 = d_dc2;
-    const int ntiles = (a.n + 127) / 128, nsm = sm_count();
-    a.ngroups = std::min(ntiles, GRAD_GROUPS * nsm);
-    a.ncta = std::min(ntiles, nsm);
+    a.ncta = std::min((a.n + 127) / 128, sm_count());
     a.status = (uint32_t*)d_workspace;
     a.nseed = a.n > 0 ? std::min(std::max((a.n + SEED_ATOMS - 1) / SEED_ATOMS, (a.R + 1023) / 1024), MAX_SEED) : 0;
     a.part2 = (double*)(a.status + MAX_SM);
     a.colpart = a.part2 + MAX_SEED;
-    a.part = (float*)(a.colpart + (size_t)a.ngroups * 4 * 128);
-    a.gat = a.part + (size_t)a.ngroups * PART;
+    a.part = (float*)(a.colpart + (size_t)a.ncta * 4 * 128);
+    a.gat = a.part + (size_t)a.ncta * PART;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
         CUtensorMap map;
