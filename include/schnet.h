@@ -358,24 +358,21 @@ SCHNET_API schnet_status schnet_get_features(schnet_ctx *ctx, uint8_t *d_codes, 
 SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, const float *h_c1, const float *h_R2,
                                             float c2);
 
-/* Readout weights on the device: R1 [F][F/2], c1, R2 [F/2], c2 [1], float32. */
-typedef struct {
-    const float *R1, *c1, *R2, *c2;
-} schnet_readout;
-
 /* Readout energies from stored features: eps_i = ssp(x_i R1 + c1) R2 + c2 with x_i
  * the stored value, E_r = sum of eps_i over o_r <= i < o_{r+1} (formed in float64,
  * rounded once; 0 for an empty replica).
  *   d_codes [n_atoms][W], d_scales [n_atoms] as stored above
  *   d_replica_offsets: device int32 [n_replicas+1], 0 <= o_0 <= ... <= o_R <= n_atoms
  *     (values outside [0, n_atoms] are read as the nearer end)
+ *   d_R1 [F][F/2], d_c1, d_R2 [F/2], d_c2 [1]: the readout's weights, device float32
  *   d_energy: device float32 [n_replicas]; d_eps: device float32 [n_atoms]; entries
  *     of atoms in no replica are written too
  *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
  * Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
 SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
-                                               const int32_t *d_replica_offsets, const schnet_readout *w,
+                                               const int32_t *d_replica_offsets, const float *d_R1,
+                                               const float *d_c1, const float *d_R2, const float *d_c2,
                                                float *d_energy, float *d_eps, void *d_workspace, size_t ws_bytes,
                                                void *cuda_stream);
 
@@ -389,7 +386,8 @@ SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uin
  * Arguments and errors otherwise as schnet_readout_energy. */
 SCHNET_API schnet_status schnet_readout_gradients(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                   int32_t n_features, int32_t n_replicas,
-                                                  const int32_t *d_replica_offsets, const schnet_readout *w,
+                                                  const int32_t *d_replica_offsets, const float *d_R1,
+                                                  const float *d_c1, const float *d_R2, const float *d_c2,
                                                   const float *d_grad_energy, float *d_dR1, float *d_dc1,
                                                   float *d_dR2, float *d_dc2, void *d_workspace, size_t ws_bytes,
                                                   void *cuda_stream);

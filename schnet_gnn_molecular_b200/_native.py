@@ -51,10 +51,6 @@ class StepParams(C.Structure):
                 ("d_noise", C.c_void_p), ("resume", C.c_int32), ("use_graph", C.c_int32)]
 
 
-class Readout(C.Structure):
-    _fields_ = [(k, C.c_void_p) for k in ("R1", "c1", "R2", "c2")]
-
-
 _lib = None
 
 
@@ -90,9 +86,8 @@ def load() -> C.CDLL:
     L.schnet_store_features.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp]
     L.schnet_get_features.argtypes = [vp, vp, vp]
     L.schnet_set_readout.argtypes = [vp, vp, vp, vp, C.c_float]
-    L.schnet_readout_energy.argtypes = [vp, vp, i32, i32, i32, vp, C.POINTER(Readout), vp, vp, vp, sz, vp]
-    L.schnet_readout_gradients.argtypes = [vp, vp, i32, i32, i32, vp, C.POINTER(Readout), vp, vp, vp, vp, vp, vp, sz,
-                                           vp]
+    L.schnet_readout_energy.argtypes = [vp, vp, i32, i32, i32] + [vp] * 8 + [sz, vp]
+    L.schnet_readout_gradients.argtypes = [vp, vp, i32, i32, i32] + [vp] * 11 + [sz, vp]
     L.schnet_readout_workspace_bytes.argtypes = [i32, i32, szp]
     L.schnet_preference_loss.argtypes = [vp, vp, i32, i32, vp, i64, C.c_double, C.c_double, vp, vp, vp, vp, vp, sz, vp]
     L.schnet_preference_workspace_bytes.argtypes = [i32, i64, szp]

@@ -76,71 +76,119 @@ __device__ __forceinline__ void pair_loss(double m, double s, double& loss, doub
     c = s - sneg;                                  // = sigma(m) - (1 - s), no cancellation at s = 0
 }
 
+// The units of the two words, and the border between them.
+struct Units {
+    double u0, u1, border;
+    __device__ explicit Units(const PrefArgs& a) : u0(power(a.s0)), u1(power(a.s1)), border(power(24 - a.s0)) {}
+    static __device__ double power(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
+};
+
+// One pair: margin out, slope into the words, loss and count to the thread's sums.
 template <class T>
-__global__ void __launch_bounds__(PT) k_pref_pairs(PrefArgs a)
+__device__ __forceinline__ void one_pair(const PrefArgs& a, const Units& u, long long p, unsigned long long* w0,
+                                         unsigned long long* w1, unsigned char* bad, double& loss, long long& count,
+                                         unsigned int& flags)
 {
-    double loss = 0.0;
-    long long count = 0;
-    unsigned int flags = 0;
-    const double u0 = __longlong_as_double((long long)(1023 + a.s0) << 52);
-    const double u1 = __longlong_as_double((long long)(1023 + a.s1) << 52);
-    const double small = __longlong_as_double((long long)(1023 + 24 - a.s0) << 52);
-    for (long long p = (long long)blockIdx.x * PT + threadIdx.x; p < a.P; p += (long long)gridDim.x * PT) {
-        const int2 q = __ldg(a.pairs + p);
-        double m, l, c;
-        const bool ok = pair_margin<T>(a, q, m, flags);
-        if (a.margins) a.margins[p] = (float)m;
-        if (!ok) continue;
-        pair_loss(m, a.s, l, c);
-        loss += l;
-        count += 1;
-        if (isnan(m)) {
-            flags |= SCHNET_FLAG_NONFINITE;
-            a.bad[q.x] = 1;
-            a.bad[q.y] = 1;
-            continue;
-        }
-        const bool fine = fabs(c) < small;
-        const long long v = __double2ll_rn(c * (fine ? u1 : u0));
-        unsigned long long* w = fine ? a.w1 : a.w0;
-        if (v != 0 && q.x != q.y) {
-            atomicAdd(w + q.x, (unsigned long long)(-v));
-            atomicAdd(w + q.y, (unsigned long long)v);
-        }
+    const int2 q = __ldg(a.pairs + p);
+    double m, l, c;
+    const bool ok = pair_margin<T>(a, q, m, flags);
+    if (a.margins) a.margins[p] = (float)m;
+    if (!ok) return;
+    pair_loss(m, a.s, l, c);
+    loss += l;
+    count += 1;
+    if (isnan(m)) {
+        flags |= SCHNET_FLAG_NONFINITE;
+        bad[q.x] = 1;
+        bad[q.y] = 1;
+        return;
     }
-    // the CTA's sums in a fixed order
-    __shared__ double sl[PT / 32];
-    __shared__ long long sc[PT / 32];
-    __shared__ unsigned int sf[PT / 32];
+    const bool fine = fabs(c) < u.border;
+    const long long v = __double2ll_rn(c * (fine ? u.u1 : u.u0));
+    unsigned long long* w = fine ? w1 : w0;
+    if (v != 0 && q.x != q.y) {
+        atomicAdd(w + q.x, (unsigned long long)(-v));
+        atomicAdd(w + q.y, (unsigned long long)v);
+    }
+}
+
+__device__ __forceinline__ float slope_of(const PrefArgs& a, double scale, unsigned long long w0, unsigned long long w1,
+                                          unsigned char bad)
+{
+    if (bad) return __int_as_float(0x7fffffff);
+    return (float)(((double)(long long)w0 * Units::power(-a.s0) + (double)(long long)w1 * Units::power(-a.s1)) * scale);
+}
+
+// the CTA's sums in a fixed order, valid in thread 0
+template <int THREADS>
+__device__ __forceinline__ PrefPartial cta_sums(double loss, long long count, unsigned int flags)
+{
+    __shared__ PrefPartial part[THREADS / 32];
     for (int o = 16; o > 0; o >>= 1) {
         loss += __shfl_xor_sync(0xffffffffu, loss, o);
         count += __shfl_xor_sync(0xffffffffu, count, o);
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
-    if ((threadIdx.x & 31) == 0) {
-        sl[threadIdx.x >> 5] = loss;
-        sc[threadIdx.x >> 5] = count;
-        sf[threadIdx.x >> 5] = flags;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = PrefPartial{loss, count, flags, 0u};
+    __syncthreads();
+    PrefPartial t{0.0, 0, 0u, 0u};
+    if (threadIdx.x == 0)
+        for (int w = 0; w < THREADS / 32; ++w) {
+            t.loss += part[w].loss;
+            t.count += part[w].count;
+            t.flags |= part[w].flags;
+        }
+    return t;
+}
+
+template <class T>
+__global__ void __launch_bounds__(PT) k_pref_pairs(PrefArgs a)
+{
+    pdl_trigger();
+    double loss = 0.0;
+    long long count = 0;
+    unsigned int flags = 0;
+    const Units u(a);
+    for (long long p = (long long)blockIdx.x * PT + threadIdx.x; p < a.P; p += (long long)gridDim.x * PT)
+        one_pair<T>(a, u, p, a.w0, a.w1, a.bad, loss, count, flags);
+    const PrefPartial t = cta_sums<PT>(loss, count, flags);
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = t;
+}
+
+// Everything in one CTA, the words in shared memory, where pairs and replicas are few
+// (SMALL_P, SMALL_R): one launch instead of three.
+constexpr int SMALL_T = 512, SMALL_P = 4096, SMALL_R = 2048;
+template <class T>
+__global__ void __launch_bounds__(SMALL_T) k_pref_small(PrefArgs a)
+{
+    __shared__ unsigned long long w0[SMALL_R], w1[SMALL_R];
+    __shared__ unsigned char bad[SMALL_R];
+    __shared__ PrefPartial total;
+    for (int r = threadIdx.x; r < a.R; r += SMALL_T) {
+        w0[r] = w1[r] = 0;
+        bad[r] = 0;
     }
     __syncthreads();
+    double loss = 0.0;
+    long long count = 0;
+    unsigned int flags = 0;
+    const Units u(a);
+    for (long long p = threadIdx.x; p < a.P; p += SMALL_T) one_pair<T>(a, u, p, w0, w1, bad, loss, count, flags);
+    const PrefPartial t = cta_sums<SMALL_T>(loss, count, flags);
+    if (threadIdx.x == 0) total = t;
+    __syncthreads();
+    const double inv = total.count > 0 ? 1.0 / (double)total.count : 0.0;
     if (threadIdx.x == 0) {
-        PrefPartial t{0.0, 0, 0u, 0u};
-        for (int w = 0; w < PT / 32; ++w) {
-            t.loss += sl[w];
-            t.count += sc[w];
-            t.flags |= sf[w];
-        }
-        a.partial[blockIdx.x] = t;
+        *a.loss = total.loss * inv;
+        if (a.flags) *a.flags = total.flags;
     }
+    for (int r = threadIdx.x; r < a.R; r += SMALL_T) a.grad[r] = slope_of(a, a.inv_kT * inv, w0[r], w1[r], bad[r]);
 }
 
 __global__ void __launch_bounds__(PT) k_pref_finish(PrefArgs a, int nparts)
 {
-    __shared__ double sl[PT];
-    __shared__ long long sc[PT];
-    __shared__ unsigned int sf;
-    if (threadIdx.x == 0) sf = 0;
-    __syncthreads();
+    pdl_wait();
+    __shared__ PrefPartial total;
     double loss = 0.0;
     long long count = 0;
     unsigned int flags = 0;
@@ -150,29 +198,16 @@ __global__ void __launch_bounds__(PT) k_pref_finish(PrefArgs a, int nparts)
         count += t.count;
         flags |= t.flags;
     }
-    sl[threadIdx.x] = loss;
-    sc[threadIdx.x] = count;
-    if (flags) atomicOr(&sf, flags);
+    const PrefPartial t = cta_sums<PT>(loss, count, flags);
+    if (threadIdx.x == 0) total = t;
     __syncthreads();
-    for (int o = PT / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) {
-            sl[threadIdx.x] += sl[threadIdx.x + o];
-            sc[threadIdx.x] += sc[threadIdx.x + o];
-        }
-        __syncthreads();
-    }
-    const double inv = sc[0] > 0 ? 1.0 / (double)sc[0] : 0.0;
+    const double inv = total.count > 0 ? 1.0 / (double)total.count : 0.0;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *a.loss = sl[0] * inv;
-        if (a.flags) *a.flags = sf;
+        *a.loss = total.loss * inv;
+        if (a.flags) *a.flags = total.flags;
     }
-    const double k0 = a.inv_kT * inv * __longlong_as_double((long long)(1023 - a.s0) << 52);
-    const double k1 = a.inv_kT * inv * __longlong_as_double((long long)(1023 - a.s1) << 52);
-    for (int r = blockIdx.x * PT + threadIdx.x; r < a.R; r += gridDim.x * PT) {
-        float g = (float)((double)(long long)a.w0[r] * k0 + (double)(long long)a.w1[r] * k1);
-        if (a.bad[r]) g = __int_as_float(0x7fffffff);
-        a.grad[r] = g;
-    }
+    for (int r = blockIdx.x * PT + threadIdx.x; r < a.R; r += gridDim.x * PT)
+        a.grad[r] = slope_of(a, a.inv_kT * inv, a.w0[r], a.w1[r], a.bad[r]);
 }
 
 static size_t pref_carve(int R, uint8_t* base, PrefArgs& a)
@@ -234,14 +269,18 @@ extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void
     a.margins = d_margins;
     a.grad = d_grad_energy;
     a.flags = d_flags;
+    const bool f64 = dtype == SCHNET_FLOAT64;
+    if (n_pairs <= SMALL_P && n_replicas <= SMALL_R) {
+        if (f64) k_pref_small<double><<<1, SMALL_T, 0, s>>>(a);
+        else k_pref_small<float><<<1, SMALL_T, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+    }
     const int g1 = (int)std::max<int64_t>(1, std::min<int64_t>((n_pairs + PT - 1) / PT, PREF_MAX_CTA));
     const int g2 = std::min((n_replicas + PT - 1) / PT, PREF_MAX_CTA);
     if (cudaMemsetAsync(d_workspace, 0, (uint8_t*)a.partial - (uint8_t*)d_workspace, s) != cudaSuccess)
         return SCHNET_ERR_CUDA;
-    if (dtype == SCHNET_FLOAT64)
-        k_pref_pairs<double><<<g1, PT, 0, s>>>(a);
-    else
-        k_pref_pairs<float><<<g1, PT, 0, s>>>(a);
-    k_pref_finish<<<g2, PT, 0, s>>>(a, g1);
+    if (f64) k_pref_pairs<double><<<g1, PT, 0, s>>>(a);
+    else k_pref_pairs<float><<<g1, PT, 0, s>>>(a);
+    if (launch_pdl(k_pref_finish, g2, PT, 0, s, a, g1) != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
 }

@@ -941,21 +941,21 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     }
 }
 
-// SMs of the current device
-static int sm_count()
+// SMs of device dev, asked for once
+static int sm_count(int dev)
 {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 1;
-    return std::min(n, MAX_SM);
+    static std::atomic<int> known[64];
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    n = std::min(n, MAX_SM);
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // more than 48 KB of shared memory for a kernel, once per device
-static bool allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& set)
+static bool allow_smem(const void* kernel, uint32_t bytes, int dev, std::atomic<uint64_t>& set)
 {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (dev < 64 && (set.load() >> dev & 1)) return true;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
     if (dev < 64) set.fetch_or((uint64_t)1 << dev);
@@ -983,17 +983,17 @@ static bool code_map(const ReadoutArgs& a, CUtensorMap* map)
 }
 
 static schnet_status readout_args(const uint8_t* codes, const uint8_t* scales, int32_t n, int32_t F, int32_t R,
-                                  const int32_t* off, const schnet_readout* w, void* ws, size_t ws_bytes,
-                                  ReadoutArgs& a)
+                                  const int32_t* off, const float* R1, const float* c1, const float* R2, const float* c2,
+                                  void* ws, size_t ws_bytes, ReadoutArgs& a)
 {
     if (F < 2 || F > FP || (F & 1)) return SCHNET_ERR_UNSUPPORTED;
     size_t need = 0;
-    if (n < 0 || R < 1 || !off || !w || !w->R1 || !w->c1 || !w->R2 || !w->c2 || !ws || ((uintptr_t)ws & 255) ||
+    if (n < 0 || R < 1 || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
         (n > 0 && (!codes || !scales || ((uintptr_t)codes & 15))) ||
         schnet_readout_workspace_bytes(n, F, &need) != SCHNET_OK || ws_bytes < need)
         return SCHNET_ERR_INVALID_ARG;
     a.codes = codes; a.scales = scales; a.n = n; a.F = F; a.H = F / 2; a.W = (F + 15) / 16 * 16; a.R = R;
-    a.off = off; a.R1 = w->R1; a.c1 = w->c1; a.R2 = w->R2; a.c2 = w->c2;
+    a.off = off; a.R1 = R1; a.c1 = c1; a.R2 = R2; a.c2 = c2;
     return SCHNET_OK;
 }
 
@@ -1035,26 +1035,28 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
 
 extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uint8_t* d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
-                                               const int32_t* d_replica_offsets, const schnet_readout* w,
+                                               const int32_t* d_replica_offsets, const float* d_R1,
+                                               const float* d_c1, const float* d_R2, const float* d_c2,
                                                float* d_energy, float* d_eps, void* d_workspace, size_t ws_bytes,
                                                void* cuda_stream)
 {
     ReadoutArgs a{};
-    schnet_status st = readout_args(d_codes, d_scales, n_atoms, n_features, n_replicas, d_replica_offsets, w,
-                                    d_workspace, ws_bytes, a);
+    schnet_status st = readout_args(d_codes, d_scales, n_atoms, n_features, n_replicas, d_replica_offsets, d_R1,
+                                    d_c1, d_R2, d_c2, d_workspace, ws_bytes, a);
     if (st != SCHNET_OK) return st;
     if (!d_energy || (n_atoms > 0 && !d_eps)) return SCHNET_ERR_INVALID_ARG;
     if (cudaPeekAtLastError() != cudaSuccess) return SCHNET_ERR_CUDA;
     a.energy = d_energy;
     a.eps = d_eps;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    const int ntiles = (a.n + 127) / 128;
-    a.ncta = std::min(ntiles, sm_count());
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SCHNET_ERR_CUDA;
+    a.ncta = std::min((a.n + 127) / 128, sm_count(dev));
     a.status = (uint32_t*)d_workspace;
     a.csum = (double*)(a.status + MAX_SM);
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, g_fwd_set))
+        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, dev, g_fwd_set))
             return SCHNET_ERR_CUDA;
         k_readout_eps<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
     }
@@ -1067,20 +1069,23 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
 
 extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const uint8_t* d_scales, int32_t n_atoms,
                                                   int32_t n_features, int32_t n_replicas,
-                                                  const int32_t* d_replica_offsets, const schnet_readout* w,
+                                                  const int32_t* d_replica_offsets, const float* d_R1,
+                                                  const float* d_c1, const float* d_R2, const float* d_c2,
                                                   const float* d_grad_energy, float* d_dR1, float* d_dc1,
                                                   float* d_dR2, float* d_dc2, void* d_workspace, size_t ws_bytes,
                                                   void* cuda_stream)
 {
     ReadoutArgs a{};
-    schnet_status st = readout_args(d_codes, d_scales, n_atoms, n_features, n_replicas, d_replica_offsets, w,
-                                    d_workspace, ws_bytes, a);
+    schnet_status st = readout_args(d_codes, d_scales, n_atoms, n_features, n_replicas, d_replica_offsets, d_R1,
+                                    d_c1, d_R2, d_c2, d_workspace, ws_bytes, a);
     if (st != SCHNET_OK) return st;
     if (!d_grad_energy || !d_dR1 || !d_dc1 || !d_dR2 || !d_dc2) return SCHNET_ERR_INVALID_ARG;
     if (cudaPeekAtLastError() != cudaSuccess) return SCHNET_ERR_CUDA;
     a.gE = d_grad_energy;
     a.dR1 = d_dR1; a.dc1 = d_dc1; a.dR2 = d_dR2; a.dc2 = d_dc2;
-    a.ncta = std::min((a.n + 127) / 128, sm_count());
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SCHNET_ERR_CUDA;
+    a.ncta = std::min((a.n + 127) / 128, sm_count(dev));
     a.status = (uint32_t*)d_workspace;
     a.nseed = a.n > 0 ? std::min(std::max((a.n + SEED_ATOMS - 1) / SEED_ATOMS, (a.R + 1023) / 1024), MAX_SEED) : 0;
     a.part2 = (double*)(a.status + MAX_SM);
@@ -1090,7 +1095,7 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_grad, GRAD_SMEM, g_grad_set))
+        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_grad, GRAD_SMEM, dev, g_grad_set))
             return SCHNET_ERR_CUDA;
         k_readout_seeds<<<a.nseed, 256, 0, s>>>(a);
         if (launch_pdl(k_readout_grad, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a) != cudaSuccess) return SCHNET_ERR_CUDA;

@@ -30,18 +30,16 @@ def test_store_refusals(lib):
 
 
 def test_readout_refusals(lib):
-    w = nat.Readout(4096, 4096, 4096, 4096)
-    no = nat.Readout(4096, None, 4096, 4096)
     big = 1 << 40
-    def energy(codes=P, scales=P, n=8, F=64, R=2, off=P, w=w, e=P, eps=P, ws=P, size=big):
-        return lib.schnet_readout_energy(codes, scales, n, F, R, off, C.byref(w) if w else None, e, eps, ws, size, None)
-    def grad(codes=P, scales=P, n=8, F=64, R=2, off=P, w=w, g=P, d=P, ws=P, size=big):
-        return lib.schnet_readout_gradients(codes, scales, n, F, R, off, C.byref(w) if w else None, g, P, P, P, d, ws,
-                                            size, None)
+    def energy(codes=P, scales=P, n=8, F=64, R=2, off=P, R1=P, c1=P, R2=P, c2=P, e=P, eps=P, ws=P, size=big):
+        return lib.schnet_readout_energy(codes, scales, n, F, R, off, R1, c1, R2, c2, e, eps, ws, size, None)
+    def grad(codes=P, scales=P, n=8, F=64, R=2, off=P, R1=P, c1=P, R2=P, c2=P, g=P, d=P, ws=P, size=big):
+        return lib.schnet_readout_gradients(codes, scales, n, F, R, off, R1, c1, R2, c2, g, P, P, P, d, ws, size, None)
     for f in (energy, grad):
         assert f(F=3) == 9 and f(F=0) == 9 and f(F=256) == 9
-        for bad in (dict(codes=None), dict(scales=None), dict(n=-1), dict(R=0), dict(off=None), dict(w=None),
-                    dict(w=no), dict(ws=None), dict(ws=C.c_void_p(4100)), dict(size=64), dict(codes=C.c_void_p(4097))):
+        for bad in (dict(codes=None), dict(scales=None), dict(n=-1), dict(R=0), dict(off=None), dict(R1=None),
+                    dict(c1=None), dict(R2=None), dict(c2=None), dict(ws=None), dict(ws=C.c_void_p(4100)),
+                    dict(size=64), dict(codes=C.c_void_p(4097))):
             assert f(**bad) == 1, (f, bad)
     assert energy(e=None) == 1 and energy(eps=None) == 1 and grad(g=None) == 1 and grad(d=None) == 1
     n = C.c_size_t(0)
