@@ -11,6 +11,9 @@
 //   word 1: the slopes below 2^(24-s0), which word 0 would keep to less than 2^-25
 //           of themselves, in units of 2^-s1, s1 = 2 s0 - 24 (|sum| < 2^62 again).
 // A pair's slope goes to one of the two words, so there are two atomics a pair.
+// A pass over the pairs is bound by its scattered accesses, one a cycle and SM whatever
+// their size: 2 gathers (the energies' gaps E - Eref are formed first) and 2 atomics.
+// 4 M pairs among 1 M replicas: 109 us with both energies gathered, 82 us so.
 #include <algorithm>
 #include <cmath>
 
@@ -20,6 +23,7 @@ namespace schnet {
 
 constexpr int PT = 256;                  // threads per CTA
 constexpr int PREF_MAX_CTA = 148 * 8;
+constexpr int PREF_N = 4;                // pairs a thread has in flight
 
 struct PrefPartial {
     double loss;
@@ -37,29 +41,26 @@ struct PrefArgs {
     double* loss;
     float *margins, *grad;
     uint32_t* flags;
-    unsigned long long *w0, *w1;         // [R] slope sums, zeroed before the pair pass
+    double* gap;                         // [R] E - Eref
+    unsigned long long *w0, *w1;         // [R] slope sums
     unsigned char* bad;                  // [R] 1: a NaN margin touches the replica
     PrefPartial* partial;                // [CTAs of the pair pass]
 };
 
-// a pair's margin; false where the pair does not count
-template <class T>
-__device__ __forceinline__ bool pair_margin(const PrefArgs& a, int2 q, double& m, unsigned int& flags)
+// whether a pair counts
+__device__ __forceinline__ bool pair_ok(const PrefArgs& a, int2 q, unsigned int& flags)
 {
-    m = 0.0;
-    if ((unsigned)q.x >= (unsigned)a.R || (unsigned)q.y >= (unsigned)a.R) {
-        if (q.x < -1 || q.x >= a.R || q.y < -1 || q.y >= a.R) flags |= SCHNET_FLAG_BADINDEX;
-        return false;
-    }
-    const T* E = static_cast<const T*>(a.energy);
-    const T* B = static_cast<const T*>(a.reference);
-    double dw = (double)__ldg(E + q.x), dl = (double)__ldg(E + q.y);
-    if (B) {
-        dw -= (double)__ldg(B + q.x);
-        dl -= (double)__ldg(B + q.y);
-    }
-    m = -(dw - dl) * a.inv_kT;
-    return true;
+    if ((unsigned)q.x < (unsigned)a.R && (unsigned)q.y < (unsigned)a.R) return true;
+    if (q.x < -1 || q.x >= a.R || q.y < -1 || q.y >= a.R) flags |= SCHNET_FLAG_BADINDEX;
+    return false;
+}
+
+// replica r's energy above the reference
+template <class T>
+__device__ __forceinline__ double gap_of(const PrefArgs& a, int r)
+{
+    const double e = (double)__ldg(static_cast<const T*>(a.energy) + r);
+    return a.reference ? e - (double)__ldg(static_cast<const T*>(a.reference) + r) : e;
 }
 
 // loss and slope of a margin: t = e^-|m|, ln(1+e^-|m|) = log1p(t), and the logistic of
@@ -83,32 +84,45 @@ struct Units {
     static __device__ double power(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
 };
 
-// One pair: margin out, slope into the words, loss and count to the thread's sums.
-template <class T>
-__device__ __forceinline__ void one_pair(const PrefArgs& a, const Units& u, long long p, unsigned long long* w0,
-                                         unsigned long long* w1, unsigned char* bad, double& loss, long long& count,
-                                         unsigned int& flags)
+// N pairs, `step` apart: margins out, slopes into the words, loss and count to the thread's
+// sums.  All of them are loaded, then all their energies, before the first is worked on:
+// the gathers' latency is what a thread waits for.
+template <int N>
+__device__ __forceinline__ void some_pairs(const PrefArgs& a, const Units& u, long long p, long long step,
+                                           const double* gap, unsigned long long* w0, unsigned long long* w1, unsigned char* bad,
+                                           double& loss, long long& count, unsigned int& flags)
 {
-    const int2 q = __ldg(a.pairs + p);
-    double m, l, c;
-    const bool ok = pair_margin<T>(a, q, m, flags);
-    if (a.margins) a.margins[p] = (float)m;
-    if (!ok) return;
-    pair_loss(m, a.s, l, c);
-    loss += l;
-    count += 1;
-    if (isnan(m)) {
-        flags |= SCHNET_FLAG_NONFINITE;
-        bad[q.x] = 1;
-        bad[q.y] = 1;
-        return;
+    int2 q[N];
+    double m[N];
+    bool ok[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) q[k] = p + k * step < a.P ? __ldg(a.pairs + p + k * step) : make_int2(-1, -1);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        ok[k] = pair_ok(a, q[k], flags);
+        m[k] = ok[k] ? (gap[q[k].y] - gap[q[k].x]) * a.inv_kT : 0.0;
     }
-    const bool fine = fabs(c) < u.border;
-    const long long v = __double2ll_rn(c * (fine ? u.u1 : u.u0));
-    unsigned long long* w = fine ? w1 : w0;
-    if (v != 0 && q.x != q.y) {
-        atomicAdd(w + q.x, (unsigned long long)(-v));
-        atomicAdd(w + q.y, (unsigned long long)v);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (a.margins && p + k * step < a.P) a.margins[p + k * step] = (float)m[k];
+        if (!ok[k]) continue;
+        double l, c;
+        pair_loss(m[k], a.s, l, c);
+        loss += l;
+        count += 1;
+        if (isnan(m[k])) {
+            flags |= SCHNET_FLAG_NONFINITE;
+            bad[q[k].x] = 1;
+            bad[q[k].y] = 1;
+            continue;
+        }
+        const bool fine = fabs(c) < u.border;
+        const long long v = __double2ll_rn(c * (fine ? u.u1 : u.u0));
+        unsigned long long* w = fine ? w1 : w0;
+        if (v != 0 && q[k].x != q[k].y) {
+            atomicAdd(w + q[k].x, (unsigned long long)(-v));
+            atomicAdd(w + q[k].y, (unsigned long long)v);
+        }
     }
 }
 
@@ -142,29 +156,43 @@ __device__ __forceinline__ PrefPartial cta_sums(double loss, long long count, un
 }
 
 template <class T>
+__global__ void __launch_bounds__(PT) k_pref_gaps(PrefArgs a)
+{
+    pdl_trigger();
+    for (int r = blockIdx.x * PT + threadIdx.x; r < a.R; r += gridDim.x * PT) {
+        a.gap[r] = gap_of<T>(a, r);
+        a.w0[r] = a.w1[r] = 0;
+        a.bad[r] = 0;
+    }
+}
+
 __global__ void __launch_bounds__(PT) k_pref_pairs(PrefArgs a)
 {
     pdl_trigger();
+    pdl_wait();
     double loss = 0.0;
     long long count = 0;
     unsigned int flags = 0;
     const Units u(a);
-    for (long long p = (long long)blockIdx.x * PT + threadIdx.x; p < a.P; p += (long long)gridDim.x * PT)
-        one_pair<T>(a, u, p, a.w0, a.w1, a.bad, loss, count, flags);
+    const long long step = (long long)gridDim.x * PT;
+    for (long long p = (long long)blockIdx.x * PT + threadIdx.x; p < a.P; p += step * PREF_N)
+        some_pairs<PREF_N>(a, u, p, step, a.gap, a.w0, a.w1, a.bad, loss, count, flags);
     const PrefPartial t = cta_sums<PT>(loss, count, flags);
     if (threadIdx.x == 0) a.partial[blockIdx.x] = t;
 }
 
 // Everything in one CTA, the words in shared memory, where pairs and replicas are few
 // (SMALL_P, SMALL_R): one launch instead of three.
-constexpr int SMALL_T = 512, SMALL_P = 4096, SMALL_R = 2048;
+constexpr int SMALL_T = 512, SMALL_P = 4096, SMALL_R = 1792;       // 42 KB + 1.8 KB of shared memory at most
 template <class T>
 __global__ void __launch_bounds__(SMALL_T) k_pref_small(PrefArgs a)
 {
-    __shared__ unsigned long long w0[SMALL_R], w1[SMALL_R];
+    extern __shared__ double small_gap[];                     // [R], then the words
+    unsigned long long *w0 = reinterpret_cast<unsigned long long*>(small_gap + a.R), *w1 = w0 + a.R;
     __shared__ unsigned char bad[SMALL_R];
     __shared__ PrefPartial total;
     for (int r = threadIdx.x; r < a.R; r += SMALL_T) {
+        small_gap[r] = gap_of<T>(a, r);
         w0[r] = w1[r] = 0;
         bad[r] = 0;
     }
@@ -173,7 +201,8 @@ __global__ void __launch_bounds__(SMALL_T) k_pref_small(PrefArgs a)
     long long count = 0;
     unsigned int flags = 0;
     const Units u(a);
-    for (long long p = threadIdx.x; p < a.P; p += SMALL_T) one_pair<T>(a, u, p, w0, w1, bad, loss, count, flags);
+    for (long long p = threadIdx.x; p < a.P; p += SMALL_T * 2)
+        some_pairs<2>(a, u, p, SMALL_T, small_gap, w0, w1, bad, loss, count, flags);
     const PrefPartial t = cta_sums<SMALL_T>(loss, count, flags);
     if (threadIdx.x == 0) total = t;
     __syncthreads();
@@ -214,6 +243,8 @@ static size_t pref_carve(int R, uint8_t* base, PrefArgs& a)
 {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     size_t off = 0;
+    a.gap = reinterpret_cast<double*>(base + off);
+    off += up((size_t)R * 8);
     a.w0 = reinterpret_cast<unsigned long long*>(base + off);
     off += up((size_t)R * 8);
     a.w1 = reinterpret_cast<unsigned long long*>(base + off);
@@ -271,16 +302,17 @@ extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void
     a.flags = d_flags;
     const bool f64 = dtype == SCHNET_FLOAT64;
     if (n_pairs <= SMALL_P && n_replicas <= SMALL_R) {
-        if (f64) k_pref_small<double><<<1, SMALL_T, 0, s>>>(a);
-        else k_pref_small<float><<<1, SMALL_T, 0, s>>>(a);
+        const size_t smem = (size_t)n_replicas * 24;
+        if (f64) k_pref_small<double><<<1, SMALL_T, smem, s>>>(a);
+        else k_pref_small<float><<<1, SMALL_T, smem, s>>>(a);
         return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
     }
     const int g1 = (int)std::max<int64_t>(1, std::min<int64_t>((n_pairs + PT - 1) / PT, PREF_MAX_CTA));
     const int g2 = std::min((n_replicas + PT - 1) / PT, PREF_MAX_CTA);
-    if (cudaMemsetAsync(d_workspace, 0, (uint8_t*)a.partial - (uint8_t*)d_workspace, s) != cudaSuccess)
+    if (f64) k_pref_gaps<double><<<g2, PT, 0, s>>>(a);
+    else k_pref_gaps<float><<<g2, PT, 0, s>>>(a);
+    if (launch_pdl(k_pref_pairs, g1, PT, 0, s, a) != cudaSuccess ||
+        launch_pdl(k_pref_finish, g2, PT, 0, s, a, g1) != cudaSuccess)
         return SCHNET_ERR_CUDA;
-    if (f64) k_pref_pairs<double><<<g1, PT, 0, s>>>(a);
-    else k_pref_pairs<float><<<g1, PT, 0, s>>>(a);
-    if (launch_pdl(k_pref_finish, g2, PT, 0, s, a, g1) != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
 }
