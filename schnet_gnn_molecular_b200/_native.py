@@ -10,6 +10,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libschnet_b200.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 OK = 0
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "CUDA", 3: "CAPACITY", 4: "SKIN", 5: "NONFINITE", 6: "BADTYPE",
@@ -51,7 +52,19 @@ class StepParams(C.Structure):
                 ("d_noise", C.c_void_p), ("resume", C.c_int32), ("use_graph", C.c_int32)]
 
 
-_lib = None
+_lib = _binding = None
+
+
+def binding():
+    """The compiled binding of the readout-tuning calls (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with `python -m schnet_gnn_molecular_b200.build`")
+        from . import _binding as module
+        _binding = module
+    return _binding
 
 
 def load() -> C.CDLL:

@@ -7,7 +7,6 @@ memory (the workspace is one uint8 tensor) and the stream.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 
 import numpy as np
 import torch
@@ -201,96 +200,34 @@ def feature_width(F: int) -> int:
     return (F + 15) // 16 * 16
 
 
-def _call(fn, i, *args):
-    """fn(*args, stream) with device i current, on its current stream."""
-    if i == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(i):
-            st = fn(*args, _raw_stream(i))
-    if st != nat.OK:
-        raise SchNetError(st, fn.__name__)
-
-
-@functools.lru_cache(maxsize=4096)
-def _scratch_bytes(name, *args):
-    n = C.c_size_t(0)
-    st = getattr(nat.load(), name)(*args, C.byref(n))
-    if st != nat.OK:
-        raise SchNetError(st, name)
-    return int(n.value)
-
-
-def _check(name, t, i, dtype, shape):
-    """t: a contiguous tensor on device i of that dtype (None: any of one byte) and shape."""
-    if (t.get_device() != i or t.shape != shape or not t.is_contiguous()
-            or (t.dtype is not dtype if dtype is not None else t.element_size() != 1)):
-        raise ValueError(f"{name} must be a contiguous tensor of {dtype or 'bytes'} and shape {tuple(shape)} on device "
-                         f"{i}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _checked(out, what):
+    """The tensors of a _binding call, or its status raised."""
+    if type(out) is int:
+        raise SchNetError(out, what)
+    return out
 
 
 def store_features(x: torch.Tensor):
     """(codes, scales) of the rows of x [n, F] (float32, float16 or bfloat16; unit column stride): e4m3 codes
     [n, feature_width(F)] (zeros past F) and one power-of-two scale a row [n]; the stored value is
     codes.float()[:, :F] * scales.float()[:, None].  See schnet_store_features in include/schnet.h."""
-    dtype, i = _STORE_DTYPES.get(x.dtype), x.get_device()
-    if i < 0 or dtype is None or x.dim() != 2:
-        raise ValueError("store_features: x must be a 2-d float32, float16 or bfloat16 CUDA tensor")
-    n, F = x.shape
-    stride, unit = x.stride()
-    if n > 0 and (unit != 1 or (n > 1 and stride < F)):
-        raise ValueError("store_features: columns must be adjacent and rows must not overlap")
-    codes = x.new_empty((n, feature_width(F)), dtype=torch.float8_e4m3fn)
-    scales = x.new_empty(n, dtype=torch.float8_e8m0fnu)
-    _call(_load().schnet_store_features, i, x.data_ptr(), dtype, n, F, max(stride, F), codes.data_ptr(),
-          scales.data_ptr())
-    return codes, scales
-
-
-def _readout_args(codes, scales, replica_offsets, readout):
-    """(device, R, F, workspace, its bytes, the leading arguments of a readout call); the workspace comes from the
-    caching allocator, so calls on different streams, or captured into different graphs, never share one."""
-    i = codes.get_device()
-    R1, c1, R2, c2 = readout["R1"], readout["c1"], readout["R2"], readout["c2"]
-    if i < 0 or codes.dim() != 2 or R1.dim() != 2 or replica_offsets.dim() != 1 or c2.numel() != 1:
-        raise ValueError("codes [n, width], R1 [F, F / 2], c2 [1] and replica_offsets [R + 1] must be CUDA tensors")
-    F, H = R1.shape
-    n, R = codes.shape[0], replica_offsets.shape[0] - 1
-    if F != 2 * H or R < 1 or n >= 2 ** 31:
-        raise ValueError(f"R1 must be [F, F / 2], is {(F, H)}; replica_offsets [R + 1] with R >= 1; fewer than 2^31 atoms")
-    _check("codes", codes, i, None, (n, feature_width(F)))
-    _check("scales", scales, i, None, (n,))
-    _check("replica_offsets", replica_offsets, i, torch.int32, (R + 1,))
-    _check("R1", R1, i, torch.float32, (F, H))
-    _check("c1", c1, i, torch.float32, (H,))
-    _check("R2", R2, i, torch.float32, (H,))
-    _check("c2", c2, i, torch.float32, c2.shape)
-    size = _scratch_bytes("schnet_readout_workspace_bytes", n, F)
-    return i, R, F, codes.new_empty(size, dtype=torch.uint8), size, (
-        codes.data_ptr(), scales.data_ptr(), n, F, R, replica_offsets.data_ptr(), R1.data_ptr(), c1.data_ptr(),
-        R2.data_ptr(), c2.data_ptr())
+    return _checked(nat.binding().store_features(x), "store_features")
 
 
 def readout_energy(codes, scales, replica_offsets, readout):
     """(energy [R], eps [n]) float32: readout energies from stored features.  replica_offsets int32 [R + 1] on the
     device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
-    i, R, _, ws, size, args = _readout_args(codes, scales, replica_offsets, readout)
-    new = readout["R1"].new_empty
-    energy, eps = new(R), new(codes.shape[0])
-    _call(_load().schnet_readout_energy, i, *args, energy.data_ptr(), eps.data_ptr(), ws.data_ptr(), size)
-    return energy, eps
+    return _checked(nat.binding().readout_energy(codes, scales, replica_offsets, readout["R1"], readout["c1"],
+                                                 readout["R2"], readout["c2"]), "readout_energy")
 
 
 def readout_gradients(codes, scales, replica_offsets, readout, grad_energy):
     """{"R1", "c1", "R2", "c2"}: gradients of sum_r grad_energy[r] E_r with respect to the readout's weights, from
     stored features; grad_energy float32 [R] (e.g. the third result of preference_loss)."""
-    i, R, F, ws, size, args = _readout_args(codes, scales, replica_offsets, readout)
-    _check("grad_energy", grad_energy, i, torch.float32, (R,))
-    new, H = grad_energy.new_empty, F // 2
-    d1, d2, d3, d4 = new((F, H)), new(H), new(H), new(1)
-    _call(_load().schnet_readout_gradients, i, *args, grad_energy.data_ptr(), d1.data_ptr(), d2.data_ptr(),
-          d3.data_ptr(), d4.data_ptr(), ws.data_ptr(), size)
-    return {"R1": d1, "c1": d2, "R2": d3, "c2": d4}
+    R1, c1, R2, c2 = _checked(nat.binding().readout_gradients(codes, scales, replica_offsets, readout["R1"],
+                                                              readout["c1"], readout["R2"], readout["c2"],
+                                                              grad_energy), "readout_gradients")
+    return {"R1": R1, "c1": c1, "R2": R2, "c2": c2}
 
 
 def preference_loss(energy, pairs, *, kT, reference=None, smoothing=0.0, flags=None):
@@ -298,30 +235,7 @@ def preference_loss(energy, pairs, *, kT, reference=None, smoothing=0.0, flags=N
     (preferred, rejected) of conformations, int32 on the device; -1 marks padding.  energy and reference: float32 or
     float64 [R]; kT in the energies' unit; flags: optional int32 [1] tensor that receives the SCHNET_FLAG_* bits of
     this call.  See schnet_preference_loss in include/schnet.h."""
-    dtype, i = _ENERGY_DTYPES.get(energy.dtype), energy.get_device()
-    if i < 0 or dtype is None or energy.dim() != 1 or energy.shape[0] < 1 or not energy.is_contiguous():
-        raise ValueError("energy must be a contiguous float32 or float64 CUDA tensor [R]")
-    R, P = energy.shape[0], pairs.shape[0]
-    _check("pairs", pairs, i, torch.int32, (P, 2))
-    if reference is not None:
-        _check("reference", reference, i, energy.dtype, (R,))
-    if flags is not None and (flags.get_device() != i or flags.numel() != 1 or flags.element_size() != 4):
-        raise ValueError("flags must be one 32-bit integer on the energies' device")
-    size = _scratch_bytes("schnet_preference_workspace_bytes", R, P)
-    ws = pairs.new_empty(size, dtype=torch.uint8)
-    loss = energy.new_empty((), dtype=torch.float64)
-    margins, grad = energy.new_empty(P, dtype=torch.float32), energy.new_empty(R, dtype=torch.float32)
-    _call(_load().schnet_preference_loss, i, energy.data_ptr(), None if reference is None else reference.data_ptr(),
-          dtype, R, pairs.data_ptr(), P, kT, smoothing, loss.data_ptr(), margins.data_ptr(), grad.data_ptr(),
-          None if flags is None else flags.data_ptr(), ws.data_ptr(), size)
-    return loss, margins, grad
-
-
-_load = nat.load
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
-    lambda i: torch.cuda.current_stream(i).cuda_stream
-_STORE_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-_ENERGY_DTYPES = {torch.float32: 0, torch.float64: 3}
+    return _checked(nat.binding().preference_loss(energy, pairs, reference, flags, kT, smoothing), "preference_loss")
 
 
 def from_workload(w, weights: dict, device=None, edge_capacity=0, weight_dtype=None) -> SchNet:

@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library ``libschnet_b200.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libschnet_b200.so`` in-tree with nvcc, and
+the Python binding of its readout-tuning calls, ``_binding.so``, with g++.
 
 Usage: ``python -m schnet_gnn_molecular_b200.build [--force] [--verbose]``.
 The library exports the C ABI declared in ``include/schnet.h``.
@@ -22,17 +23,47 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
          "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr", "-Xcompiler", "-fvisibility=hidden"]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCES = ["binding.cpp", os.path.join("..", "..", "include", "schnet.h")]
+
+
+def _stale(target: str, sources: list[str]) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.abspath(__file__)]
+    t = os.path.getmtime(target)
+    deps = [os.path.join(CSRC, s) for s in sources] + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_binding(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in (os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+                         os.path.join(cuda, "include"), sysconfig.get_paths()["include"]) for x in ("-isystem", d)],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", HERE, "-l:" + os.path.basename(LIB),
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and not _stale():
-        return LIB
+    if force or _stale(LIB, SOURCES + HEADERS):
+        _build_library(verbose, extra)
+    if force or _stale(BINDING, BINDING_SOURCES):
+        _build_binding(verbose)
+    return LIB
+
+
+def _build_library(verbose: bool, extra: list[str] | None) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [NVCC, *FLAGS, *(extra or []), "-I", os.path.join(ROOT, "include"),
            *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp, "-lcuda"]
@@ -40,7 +71,6 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -68,7 +68,7 @@ def test_context_calls_refuse_null(lib):
     assert lib.schnet_set_readout(None, P, P, P, 0.0) == 1
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_refuses_host_tensors(lib):
     x = torch.zeros(4, 64)
     with pytest.raises(ValueError):
         api.store_features(x)
