@@ -131,7 +131,7 @@ struct ReadoutArgs {
     int nseed;                           // CTAs of the seeds kernel
     float* gat;                          // [n up to a multiple of 4] g of each atom
     double* part2;                       // [nseed] shares of dc2
-    double* colpart;                     // [CTAs][4 warps][128] column sums of g sigma, g softplus / ln2
+    double* colpart;                     // [CTAs][128] column sums of g sigma, g softplus / ln2
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
@@ -279,6 +279,26 @@ __device__ __forceinline__ float row_factor(int byte, float down)
 {
     if (byte == 255 || down != down) return __int_as_float(0x7fffffff);
     return fminf(__uint_as_float((uint32_t)byte << 23) * down, 1e38f) * LOG2EF;
+}
+
+// E_r: TPR threads add the sums of the 32-atom chunks inside the replica and the single
+// atoms at its ends, in float64 and a fixed order; the sum is lane 0's of each warp.
+template <int TPR>
+__device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l)
+{
+    double s = 0.0;
+    const int lo = off_at(a, r), hi = off_at(a, r + 1);
+    const int c0 = (lo + 31) >> 5, c1 = hi >> 5;                 // whole chunks [c0, c1)
+    if (c0 < c1) {
+        for (int i = lo + l; i < c0 * 32; i += TPR) s += (double)a.eps[i];
+        for (int c = c0 + l; c < c1; c += TPR) s += a.csum[c];
+        for (int i = c1 * 32 + l; i < hi; i += TPR) s += (double)a.eps[i];
+    } else {
+        for (int i = lo + l; i < hi; i += TPR) s += (double)a.eps[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
 }
 
 // Energies.  Three groups of 8 warps and one issuing warp share the CTA's R1.  A group takes
@@ -472,8 +492,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     }
 }
 
-// E_r: TPR threads (a warp, or the CTA where replicas are long) add the sums of the 32-atom
-// chunks inside the replica and the single atoms at its ends, in float64 and a fixed order.
+// The replicas' energies: a warp each, or a CTA where replicas are long.
 template <int TPR>
 __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 {
@@ -483,20 +502,7 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
     bad = __syncthreads_or((int)bad);
     const int r = TPR == 256 ? (int)blockIdx.x : (int)(blockIdx.x * (256 / TPR) + threadIdx.x / TPR);
     const int l = threadIdx.x % TPR;
-    double s = 0.0;
-    if (r < a.R) {
-        const int lo = off_at(a, r), hi = off_at(a, r + 1);
-        const int c0 = (lo + 31) >> 5, c1 = hi >> 5;             // whole chunks [c0, c1)
-        if (c0 < c1) {
-            for (int i = lo + l; i < c0 * 32; i += TPR) s += (double)a.eps[i];
-            for (int c = c0 + l; c < c1; c += TPR) s += a.csum[c];
-            for (int i = c1 * 32 + l; i < hi; i += TPR) s += (double)a.eps[i];
-        } else {
-            for (int i = lo + l; i < hi; i += TPR) s += (double)a.eps[i];
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    double s = r < a.R ? replica_sum<TPR>(a, r, l) : 0.0;
     if (TPR == 256) {
         __shared__ double ws[8];
         if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
@@ -632,6 +638,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     const int first = (int)((long long)ntiles * blockIdx.x / a.ncta);
     const int nt = (int)((long long)ntiles * (blockIdx.x + 1) / a.ncta) - first;
     const uint32_t base = smem_u32(sm);
+    double* last = reinterpret_cast<double*>(sm + GRAD_X);       // [4][128] column sums, at the end
     auto row0 = [&](int it) { return (first + it) * 128; };
     auto fetch_tile = [&](int it) { tma_tile(base + (it & 1) * TILE_BYTES, &map, row0(it), full + (it & 1)); };
 
@@ -685,7 +692,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
         const uint64_t rhi = smem_desc(base + GRAD_R1, HP * 16, 128);
         const uint64_t rlo = smem_desc(base + GRAD_R1 + R1_TERM, HP * 16, 128);
-        float seed;
+        float seed;                                               // g and scale of this row, of the tile ahead
         int byte;
         auto load = [&](int it) {
             const int i = row0(it) + row;
@@ -877,16 +884,20 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             tc_fence_after();
             flush();
             fold();
-            if (lane < 16) {
-                double* o = a.colpart + ((size_t)blockIdx.x * 4 + wq) * 128 + part * 16 + lane;
-                o[0] = sum1;
-                o[64] = sum2;
+            if (lane < 16) {                                      // (the MMAs have read X)
+                last[wq * 128 + part * 16 + lane] = sum1;
+                last[wq * 128 + 64 + part * 16 + lane] = sum2;
             }
         }
     }
     tc_fence_before();
     const int gave_up = __syncthreads_or(!ok);
-    if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up ? 1u : 0u;
+    if (threadIdx.x < 128) {
+        const double* c = last + threadIdx.x;
+        a.colpart[(size_t)blockIdx.x * 128 + threadIdx.x] = ((c[0] + c[128]) + c[256]) + c[384];
+    } else if (threadIdx.x == 128) {
+        a.status[blockIdx.x] = gave_up ? 1u : 0u;
+    }
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -914,17 +925,19 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     } else if (b < nb + 4) {
         const double* p = a.colpart + (b - nb) * 32 + lane;
 #pragma unroll 8
-        for (int k = w; k < a.ncta * 4; k += 8) s += p[(size_t)k * 128];
-        if (b >= nb + 2)
-            for (int k = w; k < a.nseed; k += 8) s -= a.part2[k];  // ssp = softplus - ln2
-    } else {
-        for (int k = threadIdx.x; k < a.nseed; k += 256) s += a.part2[k];
+        for (int k = w; k < a.ncta; k += 8) s += p[(size_t)k * 128];
     }
     red[w][lane] = s;
     __syncthreads();
     if (w != 0) return;
     s = 0.0;
     for (int k = 0; k < 8; ++k) s += red[k][lane];
+    double total = 0.0;                                           // sum_i g_i
+    if (b >= nb + 2) {
+        for (int k = lane; k < a.nseed; k += 32) total += a.part2[k];
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        s = b < nb + 4 ? s - total : total;                       // ssp = softplus - ln2
+    }
     if (bad) s = (double)__int_as_float(0x7fffffff);
     if (b < nb) {
         const int h = b >> 2, f = (b & 3) * 32 + lane;
@@ -935,9 +948,8 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
             if (c < 64) a.dc1[h] = (float)(s * (double)a.R2[h]);
             else a.dR2[h] = (float)(s * 0.69314718055994530942);
         }
-    } else {
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) a.dc2[0] = (float)s;
+    } else if (lane == 0) {
+        a.dc2[0] = (float)s;
     }
 }
 
@@ -1028,7 +1040,7 @@ extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
     const size_t tiles = ((size_t)n_atoms + 127) / 128, ctas = std::min<size_t>(tiles, MAX_SM);
     *bytes = sizeof(uint32_t) * MAX_SM +
-             std::max(sizeof(double) * 4 * tiles, sizeof(double) * MAX_SEED + ctas * (sizeof(float) * PART + sizeof(double) * 4 * 128) +
+             std::max(sizeof(double) * 4 * tiles, sizeof(double) * MAX_SEED + ctas * (sizeof(float) * PART + sizeof(double) * 128) +
                                                       sizeof(float) * 128 * tiles);
     return SCHNET_OK;
 }
@@ -1056,8 +1068,7 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
     a.csum = (double*)(a.status + MAX_SM);
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, dev, g_fwd_set))
-            return SCHNET_ERR_CUDA;
+        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, dev, g_fwd_set)) return SCHNET_ERR_CUDA;
         k_readout_eps<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
     }
     // a warp per replica up to 4096 atoms a replica on average, else a CTA
@@ -1090,7 +1101,7 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     a.nseed = a.n > 0 ? std::min(std::max((a.n + SEED_ATOMS - 1) / SEED_ATOMS, (a.R + 1023) / 1024), MAX_SEED) : 0;
     a.part2 = (double*)(a.status + MAX_SM);
     a.colpart = a.part2 + MAX_SEED;
-    a.part = (float*)(a.colpart + (size_t)a.ncta * 4 * 128);
+    a.part = (float*)(a.colpart + (size_t)a.ncta * 128);
     a.gat = a.part + (size_t)a.ncta * PART;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
