@@ -237,42 +237,50 @@ __device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
 // a NaN of a single hidden unit).  All threads of the CTA; red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
 template <int THREADS>
-__device__ __forceinline__ float stage_r1(const ReadoutArgs& a, uint8_t* hi, uint8_t* lo, uint32_t* red)
-{
-    constexpr int PAIRS = (HP * FP / 2 + THREADS - 1) / THREADS;   // (f, f + 1) of one hidden unit each
+struct StageR1 {
+    static constexpr int PAIRS = (HP * FP / 2 + THREADS - 1) / THREADS;   // (f, f + 1) of one hidden unit each
     float v[PAIRS][2];
-    uint32_t mx = 0;                                            // as bits, which order like the magnitudes
-    if (threadIdx.x < a.H && (__float_as_uint(__ldg(a.c1 + threadIdx.x)) & 0x7fffffffu) >= 0x7f800000u) mx = 0x7f800000u;
+    uint32_t mx;                                                // as bits, which order like the magnitudes
+
+    // the loads, first thing in the kernel: what follows hides their latency
+    __device__ __forceinline__ explicit StageR1(const ReadoutArgs& a)
+    {
 #pragma unroll
-    for (int j = 0; j < PAIRS; ++j) {
-        const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
+        for (int j = 0; j < PAIRS; ++j) {
+            const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            v[j][u] = h < a.H && f + u < a.F ? __ldg(a.R1 + (f + u) * a.H + h) : 0.f;
-            mx = max(mx, __float_as_uint(v[j][u]) & 0x7fffffffu);
+            for (int u = 0; u < 2; ++u) v[j][u] = h < a.H && f + u < a.F ? __ldg(a.R1 + (f + u) * a.H + h) : 0.f;
         }
+        mx = threadIdx.x < a.H ? __float_as_uint(__ldg(a.c1 + threadIdx.x)) : 0u;
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-    __syncthreads();
-    mx = 0;
+
+    // a barrier of the whole CTA inside
+    __device__ __forceinline__ float store(uint8_t* hi, uint8_t* lo, uint32_t* red)
+    {
+        mx = (mx & 0x7fffffffu) >= 0x7f800000u ? 0x7f800000u : 0u;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) mx = max(mx, red[w]);
-    const int ex = (int)(mx >> 23);
-    int s = ex > 0 && ex < 255 ? 14 - (ex - 127) : 0;
-    s = max(-110, min(110, s));
-    const float up = __uint_as_float((uint32_t)(127 + s) << 23);
+        for (int j = 0; j < PAIRS; ++j)
+            mx = max(mx, max(__float_as_uint(v[j][0]) & 0x7fffffffu, __float_as_uint(v[j][1]) & 0x7fffffffu));
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+        __syncthreads();
+        mx = (threadIdx.x & 31) < THREADS / 32 ? red[threadIdx.x & 31] : 0u;
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const int ex = (int)(mx >> 23);
+        const int s = ex > 0 && ex < 255 ? max(-110, min(110, 14 - (ex - 127))) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + s) << 23);
 #pragma unroll
-    for (int j = 0; j < PAIRS; ++j) {
-        const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
-        if (k >= HP * FP / 2) break;
-        uint32_t vh, vl;
-        split2<0>(v[j][0] * up, v[j][1] * up, vh, vl);
-        *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
-        *reinterpret_cast<uint32_t*>(lo + kmajor_off(h, f, HP)) = vl;
+        for (int j = 0; j < PAIRS; ++j) {
+            const int k = threadIdx.x + j * THREADS, h = k % HP, f = k / HP * 2;
+            if (k >= HP * FP / 2) break;
+            uint32_t vh, vl;
+            split2<0>(v[j][0] * up, v[j][1] * up, vh, vl);
+            *reinterpret_cast<uint32_t*>(hi + kmajor_off(h, f, HP)) = vh;
+            *reinterpret_cast<uint32_t*>(lo + kmajor_off(h, f, HP)) = vl;
+        }
+        return ex == 255 ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 - s) << 23);
     }
-    return ex == 255 ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 - s) << 23);
-}
+};
 
 // the factor that takes an accumulator of row i (codes times R1 2^s) to p log2(e)
 __device__ __forceinline__ float row_factor(int byte, float down)
@@ -336,6 +344,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     auto first_row = [&](int g, int it) { return ((int)blockIdx.x + (int)gridDim.x * g + it * ngroups) * 128; };
 
     pdl_trigger();
+    StageR1<FWD_THREADS> r1(a);
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
@@ -353,13 +362,13 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 if (it < tiles_of(blockIdx.x + gridDim.x * g))
                     tma_tile(stages + (g * FWD_STAGES + it) * TILE_BYTES, &map, first_row(g, it), bars + g * FWD_NBAR + it);
     }
-    if (threadIdx.x < 32) {
-        const int h = threadIdx.x * 2;
+    if (warp == 1) {
+        const int k = threadIdx.x & 31, h = 2 * k;
         const bool i0 = h < a.H, i1 = h + 1 < a.H;
-        cst[threadIdx.x] = make_float4(i0 ? __ldg(a.c1 + h) * LOG2EF : 0.f, i1 ? __ldg(a.c1 + h + 1) * LOG2EF : 0.f,
-                                       i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
+        cst[k] = make_float4(i0 ? __ldg(a.c1 + h) * LOG2EF : 0.f, i1 ? __ldg(a.c1 + h + 1) * LOG2EF : 0.f,
+                             i0 ? __ldg(a.R2 + h) * LN2F : 0.f, i1 ? __ldg(a.R2 + h + 1) * LN2F : 0.f);
     }
-    const float down = stage_r1<FWD_THREADS>(a, sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
+    const float down = r1.store(sm + FWD_R1, sm + FWD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + FWD_RED));
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -643,6 +652,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     auto fetch_tile = [&](int it) { tma_tile(base + (it & 1) * TILE_BYTES, &map, row0(it), full + (it & 1)); };
 
     pdl_trigger();
+    StageR1<GRAD_THREADS> r1(a);
     if (warp == 0) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
@@ -659,8 +669,9 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         for (int it = 0; it < 2 && it < nt; ++it) fetch_tile(it);
     }
     float* cst = reinterpret_cast<float*>(sm + GRAD_CST);
-    if (threadIdx.x < HP) cst[threadIdx.x] = threadIdx.x < a.H ? __ldg(a.c1 + threadIdx.x) * LOG2EF : 0.f;
-    const float down = stage_r1<GRAD_THREADS>(a, sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + HP)
+        cst[threadIdx.x - 64] = (int)threadIdx.x - 64 < a.H ? __ldg(a.c1 + threadIdx.x - 64) * LOG2EF : 0.f;
+    const float down = r1.store(sm + GRAD_R1, sm + GRAD_R1 + R1_TERM, reinterpret_cast<uint32_t*>(sm + GRAD_RED));
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
