@@ -114,7 +114,7 @@ cudaError_t launch_get_features(schnet_ctx* c, uint8_t* codes, uint8_t* scales)
 // ---------------------------------------------------------------------------
 // readout energies
 // ---------------------------------------------------------------------------
-constexpr int MAX_SM = 256;              // status words: one per CTA
+constexpr int MAX_SM = 256;              // status words: one per CTA, one per thread of the kernels that sum
 
 struct ReadoutArgs {
     const uint8_t *codes, *scales;
@@ -506,16 +506,14 @@ template <int TPR>
 __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 {
     pdl_wait();
-    uint32_t bad = 0;
-    for (int k = threadIdx.x; k < a.ncta; k += 256) bad |= a.status[k];
-    bad = __syncthreads_or((int)bad);
+    uint32_t bad = (int)threadIdx.x < a.ncta ? a.status[threadIdx.x] : 0u;
     const int r = TPR == 256 ? (int)blockIdx.x : (int)(blockIdx.x * (256 / TPR) + threadIdx.x / TPR);
     const int l = threadIdx.x % TPR;
     double s = r < a.R ? replica_sum<TPR>(a, r, l) : 0.0;
+    __shared__ double ws[8];
+    if (TPR == 256 && (threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
+    bad = __syncthreads_or((int)bad);
     if (TPR == 256) {
-        __shared__ double ws[8];
-        if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = s;
-        __syncthreads();
         s = 0.0;
         for (int w = 0; w < 8; ++w) s += ws[w];
     }
@@ -924,9 +922,7 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     pdl_wait();
     __shared__ double red[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = blockIdx.x;
-    uint32_t bad = 0;
-    for (int k = threadIdx.x; k < a.ncta; k += 256) bad |= a.status[k];
-    bad = __syncthreads_or((int)bad);
+    uint32_t bad = (int)threadIdx.x < a.ncta ? a.status[threadIdx.x] : 0u;
     double s = 0.0;
     const int nb = 4 * a.H;
     if (b < nb) {
@@ -939,7 +935,7 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
         for (int k = w; k < a.ncta; k += 8) s += p[(size_t)k * 128];
     }
     red[w][lane] = s;
-    __syncthreads();
+    bad = __syncthreads_or((int)bad);
     if (w != 0) return;
     s = 0.0;
     for (int k = 0; k < 8; ++k) s += red[k][lane];
