@@ -368,7 +368,8 @@ SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, 
  *   d_energy: device float32 [n_replicas]; d_eps: device float32 [n_atoms]; entries
  *     of atoms in no replica are written too
  *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
- * Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
+ * 0 <= n_atoms <= 0x7fff0000, 1 <= n_replicas.  A NaN or an infinity in R1 or c1 makes all
+ * results NaN.  Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
 SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
                                                const int32_t *d_replica_offsets, const float *d_R1,

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
 #include <new>
 
 #include "internal.h"
@@ -787,17 +788,20 @@ schnet_status schnet_set_readout(schnet_ctx* c, const float* h_R1, const float* 
 {
     if (!c || !h_R1 || !h_c1 || !h_R2) return SCHNET_ERR_INVALID_ARG;
     Workspace& w = c->ws;
-    std::vector<uint8_t> img(2 * AW_IMG, 0);
-    std::vector<float> sc(2 * FP), v1(HP), v2(HP);
-    float v3 = 0.f;
-    pack_readout(h_R1, h_c1, h_R2, c2, c->F, c->H, img.data(), sc.data(), v1.data(), v2.data(), &v3);
+    struct Packed {
+        uint8_t img[2 * AW_IMG];
+        float sc[2 * FP], c1[HP], R2[HP], c2;
+    };
+    std::unique_ptr<Packed> p(new (std::nothrow) Packed());
+    if (!p) return fail(c, SCHNET_ERR_INVALID_ARG, "schnet_set_readout: out of host memory");
+    pack_readout(h_R1, h_c1, h_R2, c2, c->F, c->H, p->img, p->sc, p->c1, p->R2, &p->c2);
     join_in(c);
     const size_t id = 6 * (size_t)c->L;
-    CK(cudaMemcpyAsync(w.aw_img + id * AW_IMG, img.data(), img.size(), cudaMemcpyHostToDevice, c->s));
-    CK(cudaMemcpyAsync(w.aw_sc + id * FP, sc.data(), sc.size() * sizeof(float), cudaMemcpyHostToDevice, c->s));
-    CK(cudaMemcpyAsync(w.c1, v1.data(), HP * sizeof(float), cudaMemcpyHostToDevice, c->s));
-    CK(cudaMemcpyAsync(w.R2, v2.data(), HP * sizeof(float), cudaMemcpyHostToDevice, c->s));
-    CK(cudaMemcpyAsync(w.c2, &v3, sizeof(float), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.aw_img + id * AW_IMG, p->img, sizeof(p->img), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.aw_sc + id * FP, p->sc, sizeof(p->sc), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.c1, p->c1, sizeof(p->c1), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.R2, p->R2, sizeof(p->R2), cudaMemcpyHostToDevice, c->s));
+    CK(cudaMemcpyAsync(w.c2, &p->c2, sizeof(p->c2), cudaMemcpyHostToDevice, c->s));
     c->forces_valid = false;      // the stored forces are the old readout's
     CK(cudaStreamSynchronize(c->s));
     return SCHNET_OK;

@@ -181,9 +181,11 @@ __global__ void __launch_bounds__(PT) k_pref_pairs(PrefArgs a)
     if (threadIdx.x == 0) a.partial[blockIdx.x] = t;
 }
 
-// Everything in one CTA, the words in shared memory, where pairs and replicas are few
-// (SMALL_P, SMALL_R): one launch instead of three.
-constexpr int SMALL_T = 512, SMALL_P = 4096, SMALL_R = 1792;       // 42 KB + 1.8 KB of shared memory at most
+// Everything in one CTA, the words in shared memory, where pairs and replicas are few: one
+// launch instead of three.  A call takes (queued / on the device, us) 6.2 / 4.3 with 512 pairs
+// and 8.2 / 6.0 with 1024, against 10.5 / 5.2 and 10.5 / 4.7 in three; 2048 pairs, whose
+// float64 logarithms one SM works on alone, 10.3 / 9.1 against 10.5 / 4.7.
+constexpr int SMALL_T = 512, SMALL_P = 1024, SMALL_R = 1792;       // 42 KB + 1.8 KB of shared memory at most
 template <class T>
 __global__ void __launch_bounds__(SMALL_T) k_pref_small(PrefArgs a)
 {

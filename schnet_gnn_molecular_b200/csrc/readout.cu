@@ -116,6 +116,8 @@ cudaError_t launch_get_features(schnet_ctx* c, uint8_t* codes, uint8_t* scales)
 // ---------------------------------------------------------------------------
 constexpr int MAX_SM = 256;              // status words: one per CTA, one per thread of the kernels that sum
 
+constexpr int MAX_ATOMS = 0x7fff0000;    // row indexes a little past the last one stay in 32 bits
+
 struct ReadoutArgs {
     const uint8_t *codes, *scales;
     int n, F, H, W, R;
@@ -1007,7 +1009,7 @@ static schnet_status readout_args(const uint8_t* codes, const uint8_t* scales, i
 {
     if (F < 2 || F > FP || (F & 1)) return SCHNET_ERR_UNSUPPORTED;
     size_t need = 0;
-    if (n < 0 || R < 1 || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
+    if (n < 0 || n > MAX_ATOMS || R < 1 || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
         (n > 0 && (!codes || !scales || ((uintptr_t)codes & 15))) ||
         schnet_readout_workspace_bytes(n, F, &need) != SCHNET_OK || ws_bytes < need)
         return SCHNET_ERR_INVALID_ARG;
@@ -1043,7 +1045,7 @@ extern "C" schnet_status schnet_store_features(const void* d_x, int32_t dtype, i
 
 extern "C" schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t n_features, size_t* bytes)
 {
-    if (!bytes || n_atoms < 0) return SCHNET_ERR_INVALID_ARG;
+    if (!bytes || n_atoms < 0 || n_atoms > MAX_ATOMS) return SCHNET_ERR_INVALID_ARG;
     if (n_features < 2 || n_features > FP || (n_features & 1)) return SCHNET_ERR_UNSUPPORTED;
     const size_t tiles = ((size_t)n_atoms + 127) / 128, ctas = std::min<size_t>(tiles, MAX_SM);
     *bytes = sizeof(uint32_t) * MAX_SM +

@@ -6,6 +6,10 @@ products of them with R1, carried to 2^-22 or better and accumulated in fp32, on
 nearest (up to 2u a step, at most 2 F / 16 + F steps): |dp| <= (2 F + 16) 2u (|x| |R1| + |c1|) =: b.  ssp and sigma
 have slopes of at most 1 and 1/4 and are formed from a base-2 exponential and logarithm good to 2^-22, so to
 2^-20 (1 + |p|).  Sums over atoms are chains of at most 512 roundings (longer ones are cut into partial sums)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -230,6 +234,34 @@ def test_nan_rows_stay_in_their_replica():
     assert torch.isnan(bad["R1"]).all() and torch.isnan(bad["c1"]).all() and torch.isnan(bad["R2"]).all()
 
 
+@pytest.mark.parametrize("name,value", [("R1", np.nan), ("R1", np.inf), ("c1", np.nan), ("c1", -np.inf)])
+def test_nonfinite_weights_make_everything_nan(name, value):
+    rng = np.random.default_rng(15)
+    codes, scales, _ = _stored(300, 64, rng)
+    w = _weights(64, rng)
+    w[name].reshape(-1)[5] = value
+    off, g = _dev([0, 100, 300], torch.int32), _dev(np.array([1.0, -1.0], np.float32))
+    E, eps = api.readout_energy(codes, scales, off, _dw(w))
+    assert torch.isnan(E).all() and torch.isnan(eps).all()
+    got = api.readout_gradients(codes, scales, off, _dw(w), g)
+    assert torch.isnan(got["R1"]).all() and torch.isnan(got["c1"]).all() and torch.isnan(got["R2"]).all()
+
+
+def test_tiny_and_huge_weights():
+    rng = np.random.default_rng(16)
+    codes, scales, x = _stored(300, 64, rng)
+    off = [0, 100, 300]
+    for scale in (1e-20, 1e-6, 1e6):
+        w = _weights(64, rng, scale=scale)
+        E, eps = api.readout_energy(codes, scales, _dev(off, torch.int32), _dw(w))
+        assert np.all(np.abs(eps.cpu().numpy() - tuning.energy(x, off, w)[1]) <= _bounds(x, w)[3])
+    zero = {k: np.zeros_like(v) for k, v in w.items()}
+    E, eps = api.readout_energy(codes, scales, _dev(off, torch.int32), _dw(zero))
+    assert not eps.any() and not E.any()
+    got = api.readout_gradients(codes, scales, _dev(off, torch.int32), _dw(zero), _dev(np.ones(2, np.float32)))
+    assert not got["R1"].any() and not got["c1"].any() and float(got["c2"]) == 300 and not got["R2"].any()
+
+
 def test_same_inputs_same_bits():
     rng = np.random.default_rng(12)
     codes, scales, _ = _stored(30_000, 128, rng)
@@ -371,6 +403,15 @@ def test_side_stream_and_captured_graph():
         got = step(xd)
     side.synchronize()
     assert same(want, got)
+    # a tensor freed on the way is not reused by what the call itself allocates
+    free = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    del free
+    first = api.preference_loss(_dev(np.arange(300.0)), _dev([[k, 299 - k] for k in range(300)], torch.int32), kT=9.0,
+                                reference=_dev(np.arange(300.0)[::-1].copy()))
+    for _ in range(3):
+        again = api.preference_loss(_dev(np.arange(300.0)), _dev([[k, 299 - k] for k in range(300)], torch.int32),
+                                    kT=9.0, reference=_dev(np.arange(300.0)[::-1].copy()))
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
     # two graphs of the same calls, replayed on two streams at once, on other inputs
     inputs = [xd.clone(), _dev((x * 1.5).astype(np.float32))]
     wants = [step(t) for t in inputs]
@@ -487,6 +528,62 @@ def test_resume_after_set_readout_uses_the_new_forces():
         m.step(p, v, types, mass, 5, dt=2.0, gamma=0.0, step0=20, resume=resume)
         runs.append((p, v))
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    code = """
+import torch
+from schnet_gnn_molecular_b200 import api
+x = torch.arange(300 * 64, device="cuda").reshape(300, 64).float().cos()
+off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+w = {"R1": x[:64, :32].contiguous(), "c1": x[0, :32].clone(), "R2": x[1, :32].clone(), "c2": x[2, :1].clone()}
+pairs = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+def step():
+    codes, scales = api.store_features(x)
+    E, _ = api.readout_energy(codes, scales, off, w)
+    loss, _, g = api.preference_loss(E, pairs, kT=1.0)
+    return loss, api.readout_gradients(codes, scales, off, w, g)["R1"]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+want = step()
+assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=240)
+
+
+def test_the_readme_loop():
+    w = W4
+    weights = workloads.weights(w)
+    model = api.from_workload(w, weights)
+    pos, types = _dev(workloads.positions(w)), _dev(workloads.types(w), torch.int32)
+    frames = []
+    for k in range(3):                            # frames of three evaluations, concatenated
+        p = (pos * (1.0 + 0.01 * k)).contiguous()
+        model.build_neighbors(p)
+        model.energy_forces(p, types, forces=False)
+        frames.append(model.features())
+    codes, scales = torch.cat([c for c, _ in frames]), torch.cat([s for _, s in frames])
+    off = np.concatenate([[0]] + [w.replica_offsets()[1:] + k * w.n_atoms for k in range(3)]).astype(np.int32)
+    offsets, readout = _dev(off), _dw(_readout_of(weights))
+    pairs = _dev([[r, r + 4] for r in range(8)], torch.int32)
+    reference, _ = api.readout_energy(codes, scales, offsets, readout)
+    for _ in range(3):
+        E, _ = api.readout_energy(codes, scales, offsets, readout)
+        loss, margins, dE = api.preference_loss(E, pairs, kT=0.5962, reference=reference, smoothing=0.05)
+        grads = api.readout_gradients(codes, scales, offsets, readout, dE)
+        for k in readout:
+            readout[k] -= 1e-3 * grads[k]
+    x = codes.double().cpu().numpy()[:, :w.F] * scales.double().cpu().numpy()[:, None]
+    host = {k: v.cpu().numpy() for k, v in readout.items()}
+    E, _ = api.readout_energy(codes, scales, offsets, readout)
+    want, eps = tuning.energy(x, off, host)
+    scale = np.array([np.abs(eps[off[r]:off[r + 1]]).sum() for r in range(len(off) - 1)])
+    assert np.all(np.abs(E.cpu().numpy() - want) <= 1e-5 * scale)
+    model.set_readout(readout)
 
 
 def test_set_readout_refusals():

@@ -37,7 +37,8 @@ def test_readout_refusals(lib):
         return lib.schnet_readout_gradients(codes, scales, n, F, R, off, R1, c1, R2, c2, g, P, P, P, d, ws, size, None)
     for f in (energy, grad):
         assert f(F=3) == 9 and f(F=0) == 9 and f(F=256) == 9
-        for bad in (dict(codes=None), dict(scales=None), dict(n=-1), dict(R=0), dict(off=None), dict(R1=None),
+        for bad in (dict(codes=None), dict(scales=None), dict(n=-1), dict(n=2 ** 31 - 1), dict(R=0), dict(off=None),
+                    dict(R1=None),
                     dict(c1=None), dict(R2=None), dict(c2=None), dict(ws=None), dict(ws=C.c_void_p(4100)),
                     dict(size=64), dict(codes=C.c_void_p(4097))):
             assert f(**bad) == 1, (f, bad)
