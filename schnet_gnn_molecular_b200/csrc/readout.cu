@@ -4,7 +4,8 @@
 //
 // Store: per row (at most 128 features, one block) the scale is a power of two, so
 // x / scale is exact and the e4m3 rounding is the only one: codes are a function of
-// x alone, whatever computes them.
+// x alone, whatever computes them.  It is bound by HBM: 641 bytes a float32 row of 128,
+// 10^6 rows in 105 us (93 % of a copy's rate).
 #include <algorithm>
 #include <atomic>
 
@@ -115,7 +116,6 @@ cudaError_t launch_get_features(schnet_ctx* c, uint8_t* codes, uint8_t* scales)
 // readout energies
 // ---------------------------------------------------------------------------
 constexpr int MAX_SM = 256;              // status words: one per CTA, one per thread of the kernels that sum
-
 constexpr int MAX_ATOMS = 0x7fff0000;    // row indexes a little past the last one stay in 32 bits
 
 struct ReadoutArgs {
@@ -220,23 +220,11 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
-// barrier of nthreads threads; true when every one of them passed true
-__device__ __forceinline__ bool group_and(int id, int nthreads, bool ok)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"((uint32_t)ok), "r"(id), "r"(nthreads)
-                 : "memory");
-    return r != 0;
-}
-
 // R1 as the MMA's B operand [64 h][128 f] (K-major core matrices), two fp16 terms of
 // R1 2^s with 2^s the power of two that brings the largest |R1| to [2^14, 2^15): hi + lo
 // carry 22 bits, and entries 2^-24 of the largest still lose nothing above 2^-39 of it.
 // Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the gradients' epilogue drops
-// a NaN of a single hidden unit).  All threads of the CTA; red: one word per warp.
+// a NaN of a single hidden unit); red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
 template <int THREADS>
 struct StageR1 {
@@ -351,7 +339,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == FWD_GROUPS * FWD_GT) {                        // the first tiles are on their way before R1 is read
+    if (threadIdx.x == FWD_GROUPS * FWD_GT) {                     // the first tiles are on their way before R1 is stored
         for (int g = 0; g < FWD_GROUPS; ++g) {
             uint64_t* full = bars + g * FWD_NBAR;
             for (int k = 0; k < FWD_STAGES; ++k) mbar_init(full + k, 1);
@@ -546,7 +534,9 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // sums in global memory every GRAD_FLUSH tiles in any case, and the column sums are folded
 // into float64 every GRAD_FOLD tiles.
 // Bound: 3 transcendentals per hidden unit on the MUFU, 12 cycles an atom and SM (MMAs: 8,
-// shared memory: 10, HBM: 5.8).
+// shared memory: 10, HBM: 5.8).  It takes 24: its 20 warps issue every second cycle, each
+// waiting ~10 cycles an instruction (without its transcendentals 353 us for 373 at 4.2 M
+// atoms), and registers and shared memory hold no more of them.
 constexpr int GRAD_EPI = 512, GRAD_THREADS = GRAD_EPI + 128, GRAD_XS = 3;
 constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
 constexpr uint32_t GRAD_OP = 128 * 128 * 2;                      // codes as fp16 [128][128], or [128][64 hi | 64 residual]
@@ -561,7 +551,7 @@ constexpr uint32_t GRAD_MAX = GRAD_BYTE + GRAD_XS * 128;         // uint32[GRAD_
 constexpr uint32_t GRAD_BAR = GRAD_MAX + GRAD_XS * 16;
 constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * 10 + 16;
 static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
-constexpr int PART = HP * FP;                                    // one group's D2 sums, [h][f]
+constexpr int PART = HP * FP;                                    // a CTA's D2 sums, [h][f]
 
 // sums of v[0..15] over the warp's lanes: lanes c and c + 16 get column c's
 __device__ __forceinline__ float fold_columns(float (&v)[16])
@@ -588,7 +578,9 @@ __device__ __forceinline__ float rcp_mufu(float x)
 
 // Seeds: gat[i] = g of atom i's replica (0 outside all replicas), and a CTA's share of
 // dc2 = sum_r g_r times the replica's atoms.  A thread takes 4 consecutive atoms: one
-// bisection for the first, steps from there (runs of empty replicas included).
+// bisection for the first, from there the next replica or another bisection.  Looked up
+// inside the gradient kernel instead, the seeds held up its widening warps (410 us for 373
+// at 4.2 M atoms) and saved 0.3 us at 269.
 constexpr int SEED_ATOMS = 1024;         // atoms a CTA of 256 threads takes at a time
 constexpr int MAX_SEED = 1184;           // its CTAs
 __global__ void __launch_bounds__(256) k_readout_seeds(ReadoutArgs a)
@@ -598,18 +590,27 @@ __global__ void __launch_bounds__(256) k_readout_seeds(ReadoutArgs a)
     for (long long c = (long long)blockIdx.x * SEED_ATOMS; c < a.n; c += (long long)gridDim.x * SEED_ATOMS) {
         const int i0 = (int)c + threadIdx.x * 4;
         if (i0 >= a.n) continue;
-        int lo = 0, hi = a.R;                                    // the last r with o_r <= i0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (off_at(a, mid) <= i0) lo = mid; else hi = mid;
-        }
-        int next = off_at(a, lo + 1);
+        auto bisect = [&](int lo, int i) {                       // the last r >= lo with o_r <= i
+            int hi = a.R;
+            while (hi - lo > 1) {
+                const int mid = lo + ((hi - lo) >> 1);
+                if (off_at(a, mid) <= i) lo = mid; else hi = mid;
+            }
+            return lo;
+        };
+        int r = bisect(0, i0), next = off_at(a, r + 1);
         float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int i = i0 + k;
-            while (next <= i && lo < a.R - 1) next = off_at(a, ++lo + 1);
-            v[k] = i >= begin && i < end ? __ldg(a.gE + lo) : 0.f;
+            if (next <= i && r < a.R - 1) {
+                next = off_at(a, ++r + 1);
+                if (next <= i) {
+                    r = bisect(r, i);
+                    next = off_at(a, r + 1);
+                }
+            }
+            v[k] = i >= begin && i < end ? __ldg(a.gE + r) : 0.f;
         }
         *reinterpret_cast<float4*>(a.gat + i0) = make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -657,7 +658,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == GRAD_EPI) {                                // the first tiles are on their way before R1 is read
+    if (threadIdx.x == GRAD_EPI) {                                // the first tiles are on their way before R1 is stored
         for (int k = 0; k < 2; ++k) {
             mbar_init(full + k, 1);
             mbar_init(ready1 + k, 4);

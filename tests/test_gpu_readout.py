@@ -555,7 +555,7 @@ assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=240)
 
 
-def test_the_readme_loop():
+def test_a_tuning_loop_over_frames():
     w = W4
     weights = workloads.weights(w)
     model = api.from_workload(w, weights)
