@@ -529,10 +529,11 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // A and D1 are doubled, X (the codes in shared memory) is held three times and B (the
 // pairs) twice: every wait is for something handed over a tile earlier.
 // The pair's power-of-two scale 2^E brings the largest |g_i scale_i| seen so far to
-// [2^13, 2^14); when a tile has a larger one, D2 is emptied first and E lowered.  The
-// tensor core's fp32 accumulation does not round to nearest, so D2 is emptied into fp32
-// sums in global memory every GRAD_FLUSH tiles in any case, and the column sums are folded
-// into float64 every GRAD_FOLD tiles.
+// [2^13, 2^14); when a tile has a larger one, E is lowered and the tile goes to another D2.
+// The tensor core's fp32 accumulation does not round to nearest, so that happens every
+// GRAD_FLUSH tiles in any case; the D2 left is emptied into fp32 sums in global memory a
+// tile later, when its MMAs are long done.  The column sums are folded into float64 every
+// GRAD_FOLD tiles.
 // Bound: 3 transcendentals per hidden unit on the MUFU, 12 cycles an atom and SM (MMAs: 8,
 // shared memory: 10, HBM: 5.8).  It takes 24: its 20 warps issue every second cycle, each
 // waiting ~10 cycles an instruction (without its transcendentals 353 us for 373 at 4.2 M
@@ -548,6 +549,7 @@ constexpr uint32_t GRAD_RED = GRAD_CST + 64 * 4;
 constexpr uint32_t GRAD_SEED = GRAD_RED + 128;                   // float[GRAD_XS][128]: the rows' seeds
 constexpr uint32_t GRAD_BYTE = GRAD_SEED + GRAD_XS * 128 * 4;    // uint8[GRAD_XS][128]: their scales
 constexpr uint32_t GRAD_MAX = GRAD_BYTE + GRAD_XS * 128;         // uint32[GRAD_XS][4]: largest finite |g scale| of a warp
+static_assert(GRAD_MAX % 16 == 0, "read 16 bytes at a time");
 constexpr uint32_t GRAD_BAR = GRAD_MAX + GRAD_XS * 16;
 constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * 10 + 16;
 static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
@@ -678,17 +680,24 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     __syncthreads();
     tc_fence_after();
 
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);    // D2: 128 columns, A: 2 x 64, D1: 2 x 64
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);    // D2: 2 x 128 columns, A: 2 x 64, D1: 2 x 64
     const uint32_t tm = tmem + ((uint32_t)(wq * 32) << 16);
     bool ok = true;
-    int E = 120, held = 0;
-    // the scale of a tile, and whether D2 has to be emptied before it is added; x = tile % GRAD_XS
-    auto plan = [&](uint32_t x, int& e) {
-        const uint32_t* gm = gmax + x * 4;
-        const uint32_t mb = max(max(gm[0], gm[1]), max(gm[2], gm[3]));
-        e = E;
-        if (mb >= 0x00800000u) e = min(E, max(-120, min(120, 13 - ((int)(mb >> 23) - 127))));
-        return held >= GRAD_FLUSH || (e < E && held > 0);
+    int E = 120, held = 0, cur = 0;                               // the scale, the tiles in D2, and which D2
+    // takes note of a tile (x = tile % GRAD_XS): its scale, and whether it goes to the other D2
+    // because this one is full or of another scale
+    auto plan = [&](uint32_t x) {
+        const uint4 m = *reinterpret_cast<const uint4*>(gmax + x * 4);
+        const uint32_t mb = max(max(m.x, m.y), max(m.z, m.w));
+        const int e = mb >= 0x00800000u ? min(E, max(-120, min(120, 13 - ((int)(mb >> 23) - 127)))) : E;
+        const bool other = held >= GRAD_FLUSH || (e < E && held > 0);
+        if (other) {
+            cur ^= 1;
+            held = 0;
+        }
+        E = e;
+        ++held;
+        return other;
     };
     // tile `it`'s phase of one of the doubled barriers
     auto wait = [&](uint64_t* two, int it) {
@@ -713,7 +722,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             byte = in ? (int)__ldg(a.scales + i) : 127;
         };
         auto gemm1 = [&](int it) {
-            const uint32_t A = tmem + 128 + (it & 1) * 64, D = tmem + 256 + (it & 1) * 64;
+            const uint32_t A = tmem + 256 + (it & 1) * 64, D = tmem + 384 + (it & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < FP / 16; ++ks)                  // the small terms first
                 mma_ts(go, D, A + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
@@ -724,17 +733,14 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         };
         uint32_t x = 0, xb = 0;                                   // it % GRAD_XS, and the next GEMM2's
         auto gemm2 = [&](int it) {
-            int e;
-            if (plan(xb, e)) held = 0;
-            E = e;
+            plan(xb);
             const uint64_t xd = smem_desc(base + GRAD_X + xb * GRAD_OP, 128, 2048);
             const uint64_t bd = smem_desc(base + GRAD_B + (it & 1) * GRAD_OP, 128, 2048);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)                        // 16 atoms a step
-                mma_ss(go, tmem, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
-                       held > 0 || ks > 0 ? 1u : 0u);
+                mma_ss(go, tmem + cur * 128, xd + (uint64_t)((ks * 256) >> 4), bd + (uint64_t)((ks * 256) >> 4), id2,
+                       held > 1 || ks > 0 ? 1u : 0u);
             if (go) mma_commit(done2 + (it & 1));
-            ++held;
             xb = next(xb);
         };
         pdl_wait();                                               // the seeds
@@ -756,7 +762,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                     codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
                     codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
                 }
-                tmem_st16(tm + 128 + (it & 1) * 64 + q * 16, v);
+                tmem_st16(tm + 256 + (it & 1) * 64 + q * 16, v);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (q * 4 + c) * 2048), "r"(v[c * 4]),
@@ -806,13 +812,14 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         for (int k = 0; k < 16; ++k) acc1[k] = acc2[k] = 0.f;
         int folded = 0;
         bool emptied = false;
-        // D2 2^-E into the CTA's sums (the MMAs that wrote it have completed); an address
-        // belongs to one thread, so the order of its additions is fixed
-        auto flush = [&]() {
-            const float un = __uint_as_float((uint32_t)(127 - E) << 23);
+        // a D2 of scale 2^e into the CTA's sums (the MMAs that wrote it have completed); an
+        // address belongs to one thread, so the order of its additions is fixed
+        auto flush = [&](int which, int e) {
+            const float un = __uint_as_float((uint32_t)(127 - e) << 23);
             float hi[16], lo[16];
-            tmem_ld16(tm + part * 16, hi);
-            tmem_ld16(tm + 64 + part * 16, lo);
+            tc_fence_after();
+            tmem_ld16(tm + which * 128 + part * 16, hi);
+            tmem_ld16(tm + which * 128 + 64 + part * 16, lo);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -822,7 +829,6 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 else *o = v;
             }
             emptied = true;
-            held = 0;
         };
         auto fold = [&]() {
             sum1 += (double)fold_columns(acc1);
@@ -832,19 +838,18 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             folded = 0;
         };
         uint32_t x = 0;                                           // it % GRAD_XS
+        bool left = false;                                        // the other D2 has to be emptied, of this scale
+        int leftE = 0;
         for (int it = 0; it < nt; ++it) {
             if (!wait(done1, it)) break;
             tc_fence_after();
-            int e;
-            if (plan(x, e)) {
-                if (!wait(done2, it - 1)) break;
-                tc_fence_after();
-                flush();
-            }
-            E = e;
-            if (folded >= GRAD_FOLD) fold();
             float d[16];
-            tmem_ld16(tm + 256 + (it & 1) * 64 + part * 16, d);
+            tmem_ld16(tm + 384 + (it & 1) * 64 + part * 16, d);
+            const bool empty = left;
+            const int emptyE = leftE;
+            leftE = E;
+            left = plan(x);
+            if (folded >= GRAD_FOLD) fold();
             // the row's seed, factor and scaled seed; a NaN scale (or weights) makes them NaN,
             // a seed of 0 makes them 0 whatever the row holds
             float gi = seeds[x * 128 + row], k = 0.f, gx = 0.f;
@@ -857,6 +862,9 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             x = next(x);
             if (it >= 2 && !wait(done2, it - 2)) break;           // B is free
             tmem_ld_wait();
+            // the D2 that was left at the last tile: its last tile was it - 2.  (Left again at this
+            // tile, it is the one that this tile goes to.)
+            if (empty) flush(left ? cur : cur ^ 1, emptyE);
             // 8 hidden units, one 16-byte piece of each term, at a time
             const uint32_t to = base + GRAD_B + (it & 1) * GRAD_OP + part * 2 * 2048 + row * 16;
 #pragma unroll
@@ -889,12 +897,11 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ready2 + (it & 1));
-            ++held;
             ++folded;
         }
         if (ok && nt > 0 && wait(done2, nt - 1)) {
-            tc_fence_after();
-            flush();
+            if (left) flush(cur ^ 1, leftE);
+            flush(cur, E);
             fold();
             if (lane < 16) {                                      // (the MMAs have read X)
                 last[wq * 128 + part * 16 + lane] = sum1;
