@@ -5,7 +5,7 @@
 // Store: per row (at most 128 features, one block) the scale is a power of two, so
 // x / scale is exact and the e4m3 rounding is the only one: codes are a function of
 // x alone, whatever computes them.  It is bound by HBM: 641 bytes a float32 row of 128,
-// 10^6 rows in 105 us (93 % of a copy's rate).
+// 10^6 rows in 117 us (84 % of a copy's rate).
 #include <algorithm>
 #include <atomic>
 
@@ -310,7 +310,9 @@ __device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l
 // Bound: 2 transcendentals per hidden unit on the MUFU, 8 cycles an atom and SM (HBM: 133
 // bytes, 5.9 cycles; MMAs: 4).  Exponentials on the FMA pipe (one pair in 8, 4, 2) cost more
 // issue slots than they free on the MUFU: 180, 186, 192 us against 180 for 4.2 M atoms.
-// One thread per atom with four groups of 4 warps (96 registers): 195 us.
+// One thread per atom with four groups of 4 warps (96 registers): 195 us.  Widening warps
+// apart, D doubled (64 registers): 176 us for 171, and 1 us more for small calls.
+// 269 atoms: 8.0 us with the sums' kernel.
 constexpr int FWD_GROUPS = 3, FWD_STAGES = 3, FWD_GT = 256, FWD_THREADS = FWD_GROUPS * FWD_GT + 32;
 constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
 constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // Bound: 3 transcendentals per hidden unit on the MUFU, 12 cycles an atom and SM (MMAs: 8,
 // shared memory: 10, HBM: 5.8).  It takes 24: its 20 warps issue every second cycle, each
 // waiting ~10 cycles an instruction (without its transcendentals 353 us for 373 at 4.2 M
-// atoms), and registers and shared memory hold no more of them.
+// atoms, before D2 was doubled), and registers and shared memory hold no more of them.
+// 4.2 M atoms: 335-355 us, 383 under the power cap; 545 with every warp widening its own rows.
 constexpr int GRAD_EPI = 512, GRAD_THREADS = GRAD_EPI + 128, GRAD_XS = 3;
 constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
 constexpr uint32_t GRAD_OP = 128 * 128 * 2;                      // codes as fp16 [128][128], or [128][64 hi | 64 residual]
@@ -581,7 +584,7 @@ __device__ __forceinline__ float rcp_mufu(float x)
 // Seeds: gat[i] = g of atom i's replica (0 outside all replicas), and a CTA's share of
 // dc2 = sum_r g_r times the replica's atoms.  A thread takes 4 consecutive atoms: one
 // bisection for the first, from there the next replica or another bisection.  Looked up
-// inside the gradient kernel instead, the seeds held up its widening warps (410 us for 373
+// inside the gradient kernel instead, the seeds held up its widening warps (410 us for 377
 // at 4.2 M atoms) and saved 0.3 us at 269.
 constexpr int SEED_ATOMS = 1024;         // atoms a CTA of 256 threads takes at a time
 constexpr int MAX_SEED = 1184;           // its CTAs
