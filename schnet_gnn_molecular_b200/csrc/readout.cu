@@ -303,10 +303,11 @@ __device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l
 // every (3 gridDim)-th tile of 128 atoms, a thread one atom and half of its hidden units:
 // half its row of codes is read from the TMA stage, widened to fp16 (exact) and put into
 // tensor memory as the MMA's A operand (lane = atom), so D[atom][h] = codes . R1 comes back
-// with 32 hidden units per thread; the halves meet through shared memory.  A group widens
-// tile it+1, reads D(it) into registers, hands both on to the issuing warp and only then
-// works on D(it), which hides the MMAs.  The issuing thread blocks while the tensor core's
-// queue is full, so it does nothing else.
+// with 32 hidden units per thread; the halves meet through shared memory, on two barriers in
+// turn (the upper half may finish a tile ahead of the lower, not two: the next MMAs wait for
+// both).  A group widens tile it+1, reads D(it) into registers, hands both on to the issuing
+// warp and only then works on D(it), which hides the MMAs.  The issuing thread blocks while
+// the tensor core's queue is full, so it does nothing else.
 // Bound: 2 transcendentals per hidden unit on the MUFU, 8 cycles an atom and SM (HBM: 133
 // bytes, 5.9 cycles; MMAs: 4).  Exponentials on the FMA pipe (one pair in 8, 4, 2) cost more
 // issue slots than they free on the MUFU: 180, 186, 192 us against 180 for 4.2 M atoms.
@@ -319,7 +320,7 @@ constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: 
 constexpr uint32_t FWD_RED = FWD_CST + 32 * 16;
 constexpr uint32_t FWD_EX = FWD_RED + 128;                       // per group: float[2][128], the upper halves' sums
 constexpr uint32_t FWD_BAR = FWD_EX + FWD_GROUPS * 2 * 128 * 4;
-constexpr int FWD_NBAR = FWD_STAGES + 2;                         // per group: stages full, A ready, MMAs done
+constexpr int FWD_NBAR = FWD_STAGES + 2 + 8;                     // per group: stages full, A ready, MMAs done, [2][4] upper sums
 constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * FWD_NBAR + 16;
 
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -347,6 +348,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             for (int k = 0; k < FWD_STAGES; ++k) mbar_init(full + k, 1);
             mbar_init(full + FWD_STAGES, FWD_GT / 32);
             mbar_init(full + FWD_STAGES + 1, 1);
+            for (int k = 0; k < 8; ++k) mbar_init(full + FWD_STAGES + 2 + k, 1);
         }
         fence_mbar_init();
         for (int it = 0; it < FWD_STAGES; ++it)
@@ -398,13 +400,14 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 __syncwarp();
             }
         if (!ok && go)   // a wait gave up: let the copies and MMAs in flight end (bounded) before the memory goes
-            for (int k = 0; k < FWD_GROUPS * FWD_NBAR; ++k)
-                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(bars + k, ph, 1u << 12);
+            for (int g = 0; g < FWD_GROUPS; ++g)
+                for (int k = 0; k < FWD_STAGES + 2; ++k)
+                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_bounded(bars + g * FWD_NBAR + k, ph, 1u << 12);
     } else {
         const int g = threadIdx.x / FWD_GT, t = threadIdx.x & 127, half = (threadIdx.x >> 7) & 1;
         float* ex = reinterpret_cast<float*>(sm + FWD_EX) + g * 256;
-        const int pair = 1 + g * 4 + (warp & 3);                  // named barrier of the two warps that share atoms
         uint64_t* full = bars + g * FWD_NBAR;
+        uint64_t* pair = full + FWD_STAGES + 2 + (warp & 3);      // of the two warps that share atoms
         const uint32_t tmem = *tslot + 128 * g + ((uint32_t)((warp & 3) * 32) << 16);    // A: 64 columns, D: 64 columns
         const uint32_t stage0 = stages + g * FWD_STAGES * TILE_BYTES + t * 128;
         const int nt = tiles_of(blockIdx.x + gridDim.x * g);
@@ -449,10 +452,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             byte = scale_of(it + 1);
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + FWD_STAGES + 1, (uint32_t)it & 1u, RO_POLLS));
             tc_fence_after();
-            if (!ok) {                                            // (the other warp must not wait for this one)
-                if (half == 1) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(pair) : "memory");
-                break;
-            }
+            if (!ok) break;
             if (it + 1 < nt) widen(it + 1);                       // (the MMAs that read A are done)
             float d[32];
             tmem_ld32(tmem + 64 + half * 32, d);
@@ -472,9 +472,10 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             float e = (e0.x + e0.y) + (e1.x + e1.y);
             if (half == 1) {
                 ex[(it & 1) * 128 + t] = e;
-                asm volatile("barrier.cta.arrive %0, 64;" ::"r"(pair) : "memory");
+                __syncwarp();
+                if ((t & 31) == 0) mbar_arrive(pair + (it & 1) * 4);
             } else {
-                asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair) : "memory");
+                ok &= __all_sync(0xffffffffu, mbar_wait_bounded(pair + (it & 1) * 4, (uint32_t)(it >> 1) & 1u, RO_POLLS));
                 e += ex[(it & 1) * 128 + t];
                 if (i < a.n) a.eps[i] = e;
                 double s = i < a.n ? (double)e : 0.0;

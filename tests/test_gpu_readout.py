@@ -262,6 +262,17 @@ def test_tiny_and_huge_weights():
     assert not got["R1"].any() and not got["c1"].any() and float(got["c2"]) == 300 and not got["R2"].any()
 
 
+# A group of the energies' kernel takes 9 tiles, a CTA of the gradients' 27: the kernels' rings of stages, operands and
+# accumulators go round, and layers with fewer units than the upper warps hold run beside full ones.
+LAYOUTS["tiles"] = (500_009, [0, *range(11, 500_000, 131), 500_009])
+
+
+@pytest.mark.parametrize("F", [2, 32, 62, 64, 66, 94, 128])
+def test_many_tiles(F):
+    test_readout_energy("tiles", F)
+    test_readout_gradients("tiles", F)
+
+
 def test_same_inputs_same_bits():
     rng = np.random.default_rng(12)
     codes, scales, _ = _stored(30_000, 128, rng)
