@@ -180,6 +180,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+// N consecutive TMEM columns of this warp's 32 lanes -> N registers per thread
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[N])
+{
+    if constexpr (N == 32) {
+        tmem_ld32(taddr, r);
+    } else if constexpr (N == 16) {
+        tmem_ld16(taddr, r);
+    } else {
+        static_assert(N == 8, "8, 16 or 32 columns");
+        uint32_t* u = reinterpret_cast<uint32_t*>(r);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                     : "r"(taddr));
+    }
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -314,6 +331,10 @@ __device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l
 // One thread per atom with four groups of 4 warps (96 registers): 195 us.  Widening warps
 // apart, D doubled (64 registers): 176 us for 171, and 1 us more for small calls.
 // 269 atoms: 8.0 us with the sums' kernel.
+// FW is the width that codes and hidden layer are padded to: 64 up to 64 features (a thread
+// has 32 codes and 16 units, the MMAs half their K and N), else 128.  At 64 features the
+// 64 form takes 115 us for 4.2 M atoms against 184 of the 128 form, and 16.4 against 19 for
+// 192,000; the same choice made at run time inside one kernel cost 128 features 14 %.
 constexpr int FWD_GROUPS = 3, FWD_STAGES = 3, FWD_GT = 256, FWD_THREADS = FWD_GROUPS * FWD_GT + 32;
 constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
 constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
@@ -323,6 +344,7 @@ constexpr uint32_t FWD_BAR = FWD_EX + FWD_GROUPS * 2 * 128 * 4;
 constexpr int FWD_NBAR = FWD_STAGES + 2 + 8;                     // per group: stages full, A ready, MMAs done, [2][4] upper sums
 constexpr uint32_t FWD_SMEM = FWD_BAR + 8 * FWD_GROUPS * FWD_NBAR + 16;
 
+template <int FW>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
 k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 {
@@ -330,6 +352,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     float4* cst = reinterpret_cast<float4*>(sm + FWD_CST);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + FWD_BAR);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + FWD_GROUPS * FWD_NBAR);
+    constexpr int HW = FW / 2, HT = HW / 2;                       // hidden units: all, and a thread's
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int ntiles = (a.n + 127) / 128, ngroups = FWD_GROUPS * gridDim.x;
     const uint32_t stages = smem_u32(sm);
@@ -371,7 +394,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 
     if (warp == FWD_GROUPS * FWD_GT / 32) {
         // ---- issuing warp: every group's tiles in turn
-        const uint32_t id = idesc_f16(128, HP, 0, 0);
+        const uint32_t id = idesc_f16(128, HW, 0, 0);
         const uint64_t bhi = smem_desc(stages + FWD_R1, HP * 16, 128);
         const uint64_t blo = smem_desc(stages + FWD_R1 + R1_TERM, HP * 16, 128);
         const uint32_t tm0 = __shfl_sync(0xffffffffu, *tslot, 0), go = elect_one();
@@ -386,10 +409,10 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 tc_fence_after();
                 const uint32_t tm = tm0 + 128 * g;
 #pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)              // the small terms first
+                for (int ks = 0; ks < FW / 16; ++ks)              // the small terms first
                     mma_ts(go, tm + 64, tm + ks * 8, blo + (uint64_t)((ks * 2 * HP * 16) >> 4), id, ks > 0 ? 1u : 0u);
 #pragma unroll
-                for (int ks = 0; ks < FP / 16; ++ks)
+                for (int ks = 0; ks < FW / 16; ++ks)
                     mma_ts(go, tm + 64, tm + ks * 8, bhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id, 1u);
                 if (go) {
                     mma_commit(full + FWD_STAGES + 1);
@@ -422,17 +445,17 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + st, (uint32_t)(it / FWD_STAGES) & 1u, RO_POLLS));
             const uint32_t src = stage0 + st * TILE_BYTES;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < FW / 64; ++q) {
                 uint32_t v[16];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint4 w = lds128(src + (((half * 4 + q * 2 + c) ^ (t & 7)) << 4));
+                    const uint4 w = lds128(src + (((half * (FW / 32) + q * 2 + c) ^ (t & 7)) << 4));
                     codes_to_half(w.x, v[c * 8 + 0], v[c * 8 + 1]);
                     codes_to_half(w.y, v[c * 8 + 2], v[c * 8 + 3]);
                     codes_to_half(w.z, v[c * 8 + 4], v[c * 8 + 5]);
                     codes_to_half(w.w, v[c * 8 + 6], v[c * 8 + 7]);
                 }
-                tmem_st16(tmem + half * 32 + q * 16, v);
+                tmem_st16(tmem + half * (FW / 4) + q * 16, v);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         };
@@ -454,14 +477,14 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             tc_fence_after();
             if (!ok) break;
             if (it + 1 < nt) widen(it + 1);                       // (the MMAs that read A are done)
-            float d[32];
-            tmem_ld32(tmem + 64 + half * 32, d);
+            float d[HT];
+            tmem_ld(tmem + 64 + half * HT, d);
             tmem_ld_wait();
             if (it + 1 < nt) hand_over();
             float2 e0 = make_float2(c2, 0.f), e1 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float4 c = cst[half * 16 + j];
+            for (int j = 0; j < HT / 2; ++j) {
+                const float4 c = cst[half * (HT / 2) + j];
                 const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
                 const float2 u = make_float2(ex2_mufu(-fabsf(p.x)), ex2_mufu(-fabsf(p.y)));
                 const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
@@ -542,6 +565,9 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // waiting ~10 cycles an instruction (without its transcendentals 353 us for 373 at 4.2 M
 // atoms, before D2 was doubled), and registers and shared memory hold no more of them.
 // 4.2 M atoms: 335-355 us, 383 under the power cap; 545 with every warp widening its own rows.
+// FW as in the energies: in the 64 form a thread has 8 units, GEMM2's N is 64, and what the
+// unused half of X's features puts into D2 is not read.  At 64 features it takes 240 us for
+// 4.2 M atoms against 333 of the 128 form, and 26 against 33.5 for 192,000.
 constexpr int GRAD_EPI = 512, GRAD_THREADS = GRAD_EPI + 128, GRAD_XS = 3;
 constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
 constexpr uint32_t GRAD_OP = 128 * 128 * 2;                      // codes as fp16 [128][128], or [128][64 hi | 64 residual]
@@ -559,12 +585,13 @@ constexpr uint32_t GRAD_SMEM = GRAD_BAR + 8 * 10 + 16;
 static_assert(GRAD_SMEM <= 227 * 1024, "one CTA's shared memory");
 constexpr int PART = HP * FP;                                    // a CTA's D2 sums, [h][f]
 
-// sums of v[0..15] over the warp's lanes: lanes c and c + 16 get column c's
-__device__ __forceinline__ float fold_columns(float (&v)[16])
+// sums of v[0..N-1] over the warp's lanes: lane l gets column l mod N's
+template <int N>
+__device__ __forceinline__ float fold_columns(float (&v)[N])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 8; s > 0; s >>= 1) {
+    for (int s = N / 2; s > 0; s >>= 1) {
         const bool up = lane & s;
 #pragma unroll
         for (int k = 0; k < s; ++k) {
@@ -572,7 +599,10 @@ __device__ __forceinline__ float fold_columns(float (&v)[16])
             v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
     }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    float sum = v[0];
+#pragma unroll
+    for (int s = N; s < 32; s *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    return sum;
 }
 
 __device__ __forceinline__ float rcp_mufu(float x)
@@ -637,6 +667,7 @@ __global__ void __launch_bounds__(256) k_readout_seeds(ReadoutArgs a)
     }
 }
 
+template <int FW>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
 k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 {
@@ -648,6 +679,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     float* seeds = reinterpret_cast<float*>(sm + GRAD_SEED);
     uint8_t* bytes = sm + GRAD_BYTE;
     uint32_t* gmax = reinterpret_cast<uint32_t*>(sm + GRAD_MAX);
+    constexpr int HW = FW / 2, HT = HW / 4;                       // hidden units: all, and a thread's
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int wq = warp & 3, row = wq * 32 + lane;
     const int ntiles = (a.n + 127) / 128;
@@ -714,7 +746,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         // ---- widening warps, one row of codes a thread; the first one starts copies and MMAs
         const bool leader = warp == GRAD_EPI / 32;
         const uint32_t go = elect_one();
-        const uint32_t id1 = idesc_f16(128, HP, 0, 0), id2 = idesc_f16(128, 128, 0, 1) | (1u << 15);
+        const uint32_t id1 = idesc_f16(128, HW, 0, 0), id2 = idesc_f16(128, 2 * HW, 0, 1) | (1u << 15);
         const uint64_t rhi = smem_desc(base + GRAD_R1, HP * 16, 128);
         const uint64_t rlo = smem_desc(base + GRAD_R1 + R1_TERM, HP * 16, 128);
         float seed;                                               // g and scale of this row, of the tile ahead
@@ -728,10 +760,10 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         auto gemm1 = [&](int it) {
             const uint32_t A = tmem + 256 + (it & 1) * 64, D = tmem + 384 + (it & 1) * 64;
 #pragma unroll
-            for (int ks = 0; ks < FP / 16; ++ks)                  // the small terms first
+            for (int ks = 0; ks < FW / 16; ++ks)                  // the small terms first
                 mma_ts(go, D, A + ks * 8, rlo + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, ks > 0 ? 1u : 0u);
 #pragma unroll
-            for (int ks = 0; ks < FP / 16; ++ks)
+            for (int ks = 0; ks < FW / 16; ++ks)
                 mma_ts(go, D, A + ks * 8, rhi + (uint64_t)((ks * 2 * HP * 16) >> 4), id1, 1u);
             if (go) mma_commit(done1 + (it & 1));
         };
@@ -756,7 +788,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             const uint32_t src = base + (it & 1) * TILE_BYTES + row * 128;
             const uint32_t to = base + GRAD_X + x * GRAD_OP + row * 16;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < FW / 32; ++q) {
                 uint32_t v[16];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -810,24 +842,25 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         // ---- epilogue warps
         const int part = warp >> 2;
         float* sums = a.part + (size_t)blockIdx.x * PART;
-        float acc1[16], acc2[16];                                 // this thread's columns part * 16 + k
-        double sum1 = 0.0, sum2 = 0.0;                            // column part * 16 + lane % 16, folded
+        float acc1[HT], acc2[HT];                                 // this thread's columns part * HT + k
+        double sum1 = 0.0, sum2 = 0.0;                            // column part * HT + lane % HT, folded
 #pragma unroll
-        for (int k = 0; k < 16; ++k) acc1[k] = acc2[k] = 0.f;
+        for (int k = 0; k < HT; ++k) acc1[k] = acc2[k] = 0.f;
         int folded = 0;
         bool emptied = false;
         // a D2 of scale 2^e into the CTA's sums (the MMAs that wrote it have completed); an
         // address belongs to one thread, so the order of its additions is fixed
         auto flush = [&](int which, int e) {
             const float un = __uint_as_float((uint32_t)(127 - e) << 23);
-            float hi[16], lo[16];
+            float hi[HT], lo[HT];
             tc_fence_after();
-            tmem_ld16(tm + which * 128 + part * 16, hi);
-            tmem_ld16(tm + which * 128 + 64 + part * 16, lo);
+            if (wq * 32 >= FW) return;                            // (features that the narrow form does not have)
+            tmem_ld(tm + which * 128 + part * HT, hi);
+            tmem_ld(tm + which * 128 + HW + part * HT, lo);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                float* o = sums + (part * 16 + k) * FP + row;
+            for (int k = 0; k < HT; ++k) {
+                float* o = sums + (part * HT + k) * FP + row;
                 const float v = (hi[k] - lo[k]) * un;             // the residual is stored negated
                 if (emptied) atomicAdd(o, v);
                 else *o = v;
@@ -838,7 +871,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             sum1 += (double)fold_columns(acc1);
             sum2 += (double)fold_columns(acc2);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc1[k] = acc2[k] = 0.f;
+            for (int k = 0; k < HT; ++k) acc1[k] = acc2[k] = 0.f;
             folded = 0;
         };
         uint32_t x = 0;                                           // it % GRAD_XS
@@ -847,8 +880,8 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
         for (int it = 0; it < nt; ++it) {
             if (!wait(done1, it)) break;
             tc_fence_after();
-            float d[16];
-            tmem_ld16(tm + 384 + (it & 1) * 64 + part * 16, d);
+            float d[HT];
+            tmem_ld(tm + 384 + (it & 1) * 64 + part * HT, d);
             const bool empty = left;
             const int emptyE = leftE;
             leftE = E;
@@ -870,14 +903,14 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             // tile, it is the one that this tile goes to.)
             if (empty) flush(left ? cur : cur ^ 1, emptyE);
             // 8 hidden units, one 16-byte piece of each term, at a time
-            const uint32_t to = base + GRAD_B + (it & 1) * GRAD_OP + part * 2 * 2048 + row * 16;
+            const uint32_t to = base + GRAD_B + (it & 1) * GRAD_OP + part * (HT / 8) * 2048 + row * 16;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < HT / 8; ++q) {
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = q * 8 + 2 * j;
-                    const float2 b = *reinterpret_cast<const float2*>(cst + part * 16 + c);
+                    const float2 b = *reinterpret_cast<const float2*>(cst + part * HT + c);
                     float2 p = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
                     p = make_float2(fmaxf(p.x, -126.f), fmaxf(p.y, -126.f));
                     const float2 y = add2(make_float2(ex2_mufu(-p.x), ex2_mufu(-p.y)), dup2(1.f));
@@ -893,7 +926,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + q * 2048), "r"(h[0]), "r"(h[1]),
                              "r"(h[2]), "r"(h[3])
                              : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (8 + q) * 2048), "r"(l[0]), "r"(l[1]),
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (HW / 8 + q) * 2048), "r"(l[0]), "r"(l[1]),
                              "r"(l[2]), "r"(l[3])
                              : "memory");
             }
@@ -907,9 +940,9 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             if (left) flush(cur ^ 1, leftE);
             flush(cur, E);
             fold();
-            if (lane < 16) {                                      // (the MMAs have read X)
-                last[wq * 128 + part * 16 + lane] = sum1;
-                last[wq * 128 + 64 + part * 16 + lane] = sum2;
+            if (lane < HT) {                                      // (the MMAs have read X)
+                last[wq * 128 + part * HT + lane] = sum1;
+                last[wq * 128 + 64 + part * HT + lane] = sum2;
             }
         }
     }
@@ -939,6 +972,7 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     uint32_t bad = (int)threadIdx.x < a.ncta ? a.status[threadIdx.x] : 0u;
     double s = 0.0;
     const int nb = 4 * a.H;
+    if (b < nb && (b & 3) * 32 >= a.F) return;                    // inputs that the layer does not have
     if (b < nb) {
         const float* p = a.part + (b >> 2) * FP + (b & 3) * 32 + lane;
 #pragma unroll 8
@@ -994,7 +1028,7 @@ static bool allow_smem(const void* kernel, uint32_t bytes, int dev, std::atomic<
     if (dev < 64) set.fetch_or((uint64_t)1 << dev);
     return true;
 }
-static std::atomic<uint64_t> g_fwd_set{0}, g_grad_set{0};
+static std::atomic<uint64_t> g_fwd_set[2], g_grad_set[2];        // [narrow]
 
 // tensor map of the codes: rows of W bytes, boxes of 128 rows x 128 bytes, 128-byte swizzle
 static bool code_map(const ReadoutArgs& a, CUtensorMap* map)
@@ -1089,8 +1123,10 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
     a.csum = (double*)(a.status + MAX_SM);
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_eps, FWD_SMEM, dev, g_fwd_set)) return SCHNET_ERR_CUDA;
-        k_readout_eps<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
+        const bool narrow = a.F <= 64;
+        const auto f = narrow ? k_readout_eps<64> : k_readout_eps<128>;
+        if (!code_map(a, &map) || !allow_smem((const void*)f, FWD_SMEM, dev, g_fwd_set[narrow])) return SCHNET_ERR_CUDA;
+        f<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
     }
     // a warp per replica up to 4096 atoms a replica on average, else a CTA
     cudaError_t e = (int64_t)a.n > (int64_t)a.R * 4096 ? launch_pdl(k_readout_sums<256>, a.R, 256, 0, s, a)
@@ -1127,10 +1163,12 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     cudaStream_t s = (cudaStream_t)cuda_stream;
     if (a.n > 0) {
         CUtensorMap map;
-        if (!code_map(a, &map) || !allow_smem((const void*)k_readout_grad, GRAD_SMEM, dev, g_grad_set))
+        const bool narrow = a.F <= 64;
+        const auto f = narrow ? k_readout_grad<64> : k_readout_grad<128>;
+        if (!code_map(a, &map) || !allow_smem((const void*)f, GRAD_SMEM, dev, g_grad_set[narrow]))
             return SCHNET_ERR_CUDA;
         k_readout_seeds<<<a.nseed, 256, 0, s>>>(a);
-        if (launch_pdl(k_readout_grad, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a) != cudaSuccess) return SCHNET_ERR_CUDA;
+        if (launch_pdl(f, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a) != cudaSuccess) return SCHNET_ERR_CUDA;
     }
     if (launch_pdl(k_readout_grad_sum, 4 * a.H + 5, 256, 0, s, a) != cudaSuccess) return SCHNET_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
