@@ -368,7 +368,7 @@ SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, 
  *   d_energy: device float32 [n_replicas]; d_eps: device float32 [n_atoms]; entries
  *     of atoms in no replica are written too
  *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
- * 0 <= n_atoms <= 0x7fff0000, 1 <= n_replicas.  A NaN or an infinity in R1 or c1 makes all
+ * 0 <= n_atoms <= 0x7fff0000, 1 <= n_replicas <= 0x7ff00000.  A NaN or an infinity in R1 or c1 makes all
  * results NaN.  Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
 SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
@@ -417,7 +417,7 @@ SCHNET_API schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
  * as 64-bit integers, which add up to the same value in any order; with b the bits of
  * n_pairs, a slope is kept to 2^-25 of itself down to 2^(2b - 76) and to 2^(2b - 101)
  * below that.
- * kT > 0; 0 <= smoothing <= 1; 1 <= n_replicas; 0 <= n_pairs < 2^31.
+ * kT > 0; 0 <= smoothing <= 1; 1 <= n_replicas <= 0x7ff00000; 0 <= n_pairs < 2^31.
  * Errors: INVALID_ARG, CUDA. */
 SCHNET_API schnet_status schnet_preference_loss(const void *d_energy, const void *d_reference, int32_t dtype,
                                                 int32_t n_replicas, const int32_t *d_pairs, int64_t n_pairs,

@@ -21,6 +21,9 @@ constexpr int SCAN_BLOCK = 1024;      // threads per scan block
 constexpr int SCAN_ITEMS = 4;         // items per thread
 constexpr int SCAN_TILE = SCAN_BLOCK * SCAN_ITEMS;
 constexpr int REDUCE_CHUNK = 4096;    // atoms per partial sum of a per-replica reduction
+// Replicas of the readout-tuning calls: an index and the largest stride it is advanced by
+// (1184 CTAs of 256 threads) stay in 32 bits.
+constexpr int MAX_REPLICAS = 0x7ff00000;
 
 // Cells are at least (r_c + skin) (1 + 2^-20) wide and atoms are binned in
 // float64, so the binning's rounding (a few float64 ulps of the cell

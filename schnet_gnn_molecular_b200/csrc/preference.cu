@@ -264,7 +264,7 @@ using namespace schnet;
 
 extern "C" schnet_status schnet_preference_workspace_bytes(int32_t n_replicas, int64_t n_pairs, size_t* bytes)
 {
-    if (!bytes || n_replicas < 1 || n_pairs < 0 || n_pairs > 0x7fffffffLL) return SCHNET_ERR_INVALID_ARG;
+    if (!bytes || n_replicas < 1 || n_replicas > MAX_REPLICAS || n_pairs < 0 || n_pairs > 0x7fffffffLL) return SCHNET_ERR_INVALID_ARG;
     PrefArgs a{};
     *bytes = pref_carve(n_replicas, nullptr, a);
     return SCHNET_OK;

@@ -1055,7 +1055,7 @@ static schnet_status readout_args(const uint8_t* codes, const uint8_t* scales, i
 {
     if (F < 2 || F > FP || (F & 1)) return SCHNET_ERR_UNSUPPORTED;
     size_t need = 0;
-    if (n < 0 || n > MAX_ATOMS || R < 1 || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
+    if (n < 0 || n > MAX_ATOMS || R < 1 || R > MAX_REPLICAS || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
         (n > 0 && (!codes || !scales || ((uintptr_t)codes & 15))) ||
         schnet_readout_workspace_bytes(n, F, &need) != SCHNET_OK || ws_bytes < need)
         return SCHNET_ERR_INVALID_ARG;

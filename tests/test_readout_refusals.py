@@ -50,6 +50,23 @@ def test_readout_refusals(lib):
     assert lib.schnet_readout_workspace_bytes(1, 64, None) == 1
 
 
+# the kernels step through the replicas in 32 bits: past this many an index could wrap
+MAX_REPLICAS = 0x7ff00000
+
+
+def test_too_many_replicas(lib):
+    big = 1 << 62
+    need = C.c_size_t(0)
+    for R in (MAX_REPLICAS + 1, 2 ** 31 - 1):
+        assert lib.schnet_preference_workspace_bytes(R, 9, C.byref(need)) == 1
+        assert lib.schnet_preference_loss(P, None, 0, R, P, 9, 0.6, 0.0, P, None, P, None, P, big, None) == 1
+        assert lib.schnet_readout_energy(P, P, 8, 64, R, P, P, P, P, P, P, P, P, big, None) == 1
+        assert lib.schnet_readout_gradients(P, P, 8, 64, R, P, P, P, P, P, P, P, P, P, P, P, big, None) == 1
+    assert lib.schnet_preference_workspace_bytes(MAX_REPLICAS, 9, C.byref(need)) == 0
+    # the largest stride of a loop over replicas is 1184 CTAs of 256 threads
+    assert MAX_REPLICAS - 1 + 1184 * 256 < 2 ** 31
+
+
 def test_preference_refusals(lib):
     need = C.c_size_t(0)
     assert lib.schnet_preference_workspace_bytes(16, 9, C.byref(need)) == 0
