@@ -785,6 +785,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             if (!wait(full, it)) break;
             if (it >= 2 && !wait(done1, it - 2)) break;           // A is free
             if (it >= GRAD_XS && !wait(done2, it - GRAD_XS)) break;    // X and the rows' slots are free
+            tc_fence_after();                                     // A is overwritten after the MMAs' reads
             const uint32_t src = base + (it & 1) * TILE_BYTES + row * 128;
             const uint32_t to = base + GRAD_X + x * GRAD_OP + row * 16;
 #pragma unroll
