@@ -240,8 +240,8 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // R1 as the MMA's B operand [64 h][128 f] (K-major core matrices), two fp16 terms of
 // R1 2^s with 2^s the power of two that brings the largest |R1| to [2^14, 2^15): hi + lo
 // carry 22 bits, and entries 2^-24 of the largest still lose nothing above 2^-39 of it.
-// Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (the gradients' epilogue drops
-// a NaN of a single hidden unit); red: one word per warp.
+// Returns 2^-s, or NaN where R1 or c1 holds a NaN or an infinity (in the accumulators it would
+// reach only its own hidden unit); red: one word per warp.
 constexpr uint32_t R1_TERM = HP * FP * 2;
 template <int THREADS>
 struct StageR1 {
@@ -274,7 +274,7 @@ struct StageR1 {
         mx = (threadIdx.x & 31) < THREADS / 32 ? red[threadIdx.x & 31] : 0u;
         mx = __reduce_max_sync(0xffffffffu, mx);
         const int ex = (int)(mx >> 23);
-        const int s = ex > 0 && ex < 255 ? max(-110, min(110, 14 - (ex - 127))) : 0;
+        const int s = ex > 0 && ex < 255 ? min(110, 14 - (ex - 127)) : 0;       // -113 .. 110: 2^s and 2^-s are normal
         const float up = __uint_as_float((uint32_t)(127 + s) << 23);
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
@@ -913,7 +913,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                     const int c = q * 8 + 2 * j;
                     const float2 b = *reinterpret_cast<const float2*>(cst + part * HT + c);
                     float2 p = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
-                    p = make_float2(fmaxf(p.x, -126.f), fmaxf(p.y, -126.f));
+                    p = make_float2(max_nan(p.x, -126.f), max_nan(p.y, -126.f));
                     const float2 y = add2(make_float2(ex2_mufu(-p.x), ex2_mufu(-p.y)), dup2(1.f));
                     const float2 sg = make_float2(rcp_mufu(y.x), rcp_mufu(y.y));
                     const float2 sp2 = add2(p, make_float2(lg2_mufu(y.x), lg2_mufu(y.y)));

@@ -262,6 +262,34 @@ def test_tiny_and_huge_weights():
     assert not got["R1"].any() and not got["c1"].any() and float(got["c2"]) == 300 and not got["R2"].any()
 
 
+@pytest.mark.parametrize("F", [64, 128])
+@pytest.mark.parametrize("ex", [125, 126, 127])
+def test_weights_near_the_largest_finite(F, ex):
+    """|R1| in [2^ex, 2^(ex+1)), features of a few 2^-109: pre-activations of +-2^17 to 2^27, one sign a unit."""
+    rng = np.random.default_rng(ex)
+    n, H, off = 300, F // 2, [0, 100, 300]
+    x = np.ldexp(rng.integers(0, 8, size=(n, F)).astype(np.float64), -109)
+    codes, scales = api.store_features(_dev(x.astype(np.float32)))
+    w = _weights(F, rng)
+    sign = np.where(np.arange(H) % 3 == 0, -1.0, 1.0)
+    w["R1"] = (np.ldexp(rng.uniform(1.0, 1.99, size=(F, H)), ex) * sign).astype(np.float32)
+    E, eps = api.readout_energy(codes, scales, _dev(off, torch.int32), _dw(w))
+    want_E, want = tuning.energy(x, off, w)
+    tol = _bounds(x, w)[3]
+    assert np.all(np.abs(eps.cpu().numpy() - want) <= tol)
+    for r in range(2):
+        assert abs(float(E[r]) - want_E[r]) <= tol[off[r]:off[r + 1]].sum() + U * abs(want_E[r])
+    # one seed and one sign a unit: nothing cancels.  n / 16 steps of 17 terms, each cut off by 2u of the sum at most,
+    # beside the pre-activation's (2 F + 16) 2u and the functions' 2^-20
+    got = api.readout_gradients(codes, scales, _dev(off, torch.int32), _dw(w), _dev(np.ones(2, np.float32)))
+    want = tuning.gradients(x, off, w, np.ones(2))
+    rel = (n / 16 + 1) * 17 * 2 * U + (2 * F + 16) * 2 * U + 2.0 ** -20
+    for k in want:
+        # where a unit's pre-activations are negative: ssp's 2^-20 (1 + |p|); sigma is not below 2^-126
+        floor = n * 2.0 ** -20 * (1 + np.abs(tuning.hidden(x, w)).max(0)) if k == "R2" else n * 2.0 ** -125 * 4
+        assert np.all(np.abs(got[k].cpu().numpy() - want[k]) <= rel * np.abs(want[k]) + floor), k
+
+
 # A group of the energies' kernel takes 9 tiles, a CTA of the gradients' 27: the kernels' rings of stages, operands and
 # accumulators go round, and layers with fewer units than the upper warps hold run beside full ones.
 LAYOUTS["tiles"] = (500_009, [0, *range(11, 500_000, 131), 500_009])
