@@ -8,6 +8,7 @@
 // 10^6 rows in 107 us (92 % of a copy's rate).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -133,7 +134,7 @@ struct ReadoutArgs {
     int nseed;                           // CTAs of the seeds kernel
     float* gat;                          // [n up to a multiple of 4] g of each atom
     double* part2;                       // [nseed] shares of dc2
-    double* colpart;                     // [CTAs][128] column sums of g sigma, g softplus / ln2
+    double* colpart;                     // [CTAs][128] column sums of 2 g sigma, g ssp / ln2
 };
 
 __device__ __forceinline__ int off_at(const ReadoutArgs& a, int r) { return min(max(__ldg(a.off + r), 0), a.n); }
@@ -544,11 +545,13 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 // and scale; the first of them also starts copies and MMAs.  Sixteen epilogue warps hold
 // one atom and 16 hidden units a thread.  Per tile:
 //   GEMM1  D1[atom][h] = codes . R1 as in the energies;
-//   epilogue  per (atom, h), t = p log2(e) >= -126, y = 1 + 2^-t: sigma = 1 / y and
-//     ln(1 + e^p) = ln2 (t + log2 y), which for negative t keeps 2^-22 |t| absolutely (the
-//     same as the rounding of t); the column sums of g sigma and g (t + log2 y) stay in
-//     registers (ssp's -ln2 is dc2's share, taken off at the end), and sigma g_i scale_i
-//     goes to shared memory as an fp16 hi + residual pair;
+//   epilogue  per (atom, h), t = p log2(e) >= -126, y = 1/2 + 2^-t / 2: 2 sigma = 1 / y and
+//     ssp(p) = ln2 (t + log2 y), which has no constant offset (small pre-activations keep
+//     their bits in the sums) and for negative t keeps 2^-22 |t| absolutely (the same as the
+//     rounding of t); where a warp's 8 units of 32 atoms all have |t| <= 3, a polynomial of
+//     relative accuracy stands for it (finding that out costs 1.4 % at 4.2 M atoms); the
+//     column sums of 2 g sigma and g ssp / ln2 stay in registers, and sigma g_i scale_i goes
+//     to shared memory as an fp16 hi + residual pair;
 //   GEMM2  D2[f][h] += codes^T (sigma g scale): both operands are read MN-major, so the
 //     tile of codes widened once serves as it lies, and D2 stays in tensor memory from tile
 //     to tile.  R2 is a factor of whole columns and is applied at the very end.
@@ -610,6 +613,22 @@ __device__ __forceinline__ float rcp_mufu(float x)
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// log2((1 + 2^t) / 2) for |t| <= 3 as t / 2 and an even polynomial (ssp2_fit.py; relative error 2e-7).
+// The MUFU logarithm errs by up to 2^-22 around 1 and by 6e-8 on average: with it alone dR2 of 64
+// chains is off by 6e-6, 4e-5 and 8e-4 of itself at a tenth, hundredth and thousandth of Xavier
+// weights, with this 3e-7, 1.2e-7 and 1.2e-7 (torch's float32 forms: 6e-7, 3e-6 and 7e-5).
+constexpr float SSP2_SMALL = 3.f;
+__device__ __forceinline__ float2 ssp2_small(float2 t)
+{
+    const float2 s = mul2(t, t);
+    float2 q = fma2(dup2(-1.0950124140762796e-09f), s, dup2(6.010890274410485e-08f));
+    q = fma2(q, s, dup2(-1.9344583961355966e-06f));
+    q = fma2(q, s, dup2(5.532750947168097e-05f));
+    q = fma2(q, s, dup2(-0.0017342476639896631f));
+    q = fma2(q, s, dup2(0.08664331585168839f));
+    return mul2(t, fma2(t, q, dup2(0.5f)));
 }
 
 // Seeds: gat[i] = g of atom i's replica (0 outside all replicas), and a CTA's share of
@@ -895,7 +914,7 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 const int byte = bytes[x * 128 + row];
                 k = row_factor(byte, down);
                 if (k != k) gi = k;
-                gx = gi * __uint_as_float((uint32_t)byte << 23) * __uint_as_float((uint32_t)(127 + E) << 23);
+                gx = gi * __uint_as_float((uint32_t)byte << 23) * __uint_as_float((uint32_t)(126 + E) << 23);   // half: of 2 sigma
             }
             x = next(x);
             if (it >= 2 && !wait(done2, it - 2)) break;           // B is free
@@ -908,19 +927,25 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 #pragma unroll
             for (int q = 0; q < HT / 8; ++q) {
                 uint32_t h[4], l[4];
+                float2 t[4];
+                float most = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = q * 8 + 2 * j;
                     const float2 b = *reinterpret_cast<const float2*>(cst + part * HT + c);
-                    float2 p = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
-                    p = make_float2(max_nan(p.x, -126.f), max_nan(p.y, -126.f));
-                    const float2 y = add2(make_float2(ex2_mufu(-p.x), ex2_mufu(-p.y)), dup2(1.f));
-                    const float2 sg = make_float2(rcp_mufu(y.x), rcp_mufu(y.y));
-                    const float2 sp2 = add2(p, make_float2(lg2_mufu(y.x), lg2_mufu(y.y)));
+                    t[j] = fma2(make_float2(d[c], d[c + 1]), dup2(k), b);
+                    t[j] = make_float2(max_nan(t[j].x, -126.f), max_nan(t[j].y, -126.f));
+                    most = fmaxf(fmaxf(most, fabsf(t[j].x)), fabsf(t[j].y));
+                }
+                const bool small = __all_sync(0xffffffffu, most <= SSP2_SMALL);
+                float2 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = q * 8 + 2 * j;
+                    y[j] = fma2(dup2(0.5f), make_float2(ex2_mufu(-t[j].x), ex2_mufu(-t[j].y)), dup2(0.5f));
+                    const float2 sg = make_float2(rcp_mufu(y[j].x), rcp_mufu(y[j].y));        // 2 sigma
                     const float2 a1 = fma2(dup2(gi), sg, make_float2(acc1[c], acc1[c + 1]));
-                    const float2 a2 = fma2(dup2(gi), sp2, make_float2(acc2[c], acc2[c + 1]));
                     acc1[c] = a1.x; acc1[c + 1] = a1.y;
-                    acc2[c] = a2.x; acc2[c + 1] = a2.y;
                     const float2 w = mul2(dup2(gx), sg);
                     split2_neg<0>(w.x, w.y, h[j], l[j]);
                 }
@@ -930,6 +955,17 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (HW / 8 + q) * 2048), "r"(l[0]), "r"(l[1]),
                              "r"(l[2]), "r"(l[3])
                              : "memory");
+                auto sums = [&](auto poly) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = q * 8 + 2 * j;
+                        const float2 sp2 = poly ? ssp2_small(t[j]) : add2(t[j], make_float2(lg2_mufu(y[j].x), lg2_mufu(y[j].y)));
+                        const float2 a2 = fma2(dup2(gi), sp2, make_float2(acc2[c], acc2[c + 1]));
+                        acc2[c] = a2.x; acc2[c + 1] = a2.y;
+                    }
+                };
+                if (small) sums(std::true_type{});
+                else sums(std::false_type{});
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -961,8 +997,8 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     }
 }
 
-// dR1 = R2_h sum of the CTAs' D2, dc1 = R2_h sum of g sigma, dR2 = ln2 (sum of
-// g softplus / ln2 - sum of g), dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
+// dR1 = R2_h sum of the CTAs' D2, dc1 = R2_h / 2 sum of 2 g sigma, dR2 = ln2 sum of g ssp / ln2,
+// dc2 = sum_r g_r times the replica's atoms; in float64, in a fixed order.  A CTA takes 32
 // columns (CTAs 0 .. 4 H - 1: R1, a quarter of the f of one h each; then 4 for c1 and R2;
 // then c2), its 8 warps a share of the partial sums each.
 __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
@@ -988,11 +1024,10 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     if (w != 0) return;
     s = 0.0;
     for (int k = 0; k < 8; ++k) s += red[k][lane];
-    double total = 0.0;                                           // sum_i g_i
-    if (b >= nb + 2) {
-        for (int k = lane; k < a.nseed; k += 32) total += a.part2[k];
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        s = b < nb + 4 ? s - total : total;                       // ssp = softplus - ln2
+    if (b == nb + 4) {                                            // sum_i g_i
+        s = 0.0;
+        for (int k = lane; k < a.nseed; k += 32) s += a.part2[k];
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
     if (bad) s = (double)__int_as_float(0x7fffffff);
     if (b < nb) {
@@ -1001,7 +1036,7 @@ __global__ void __launch_bounds__(256) k_readout_grad_sum(ReadoutArgs a)
     } else if (b < nb + 4) {
         const int c = (b - nb) * 32 + lane, h = c & 63;
         if (h < a.H) {
-            if (c < 64) a.dc1[h] = (float)(s * (double)a.R2[h]);
+            if (c < 64) a.dc1[h] = (float)(s * 0.5 * (double)a.R2[h]);
             else a.dR2[h] = (float)(s * 0.69314718055994530942);
         }
     } else if (lane == 0) {

@@ -262,6 +262,42 @@ def test_tiny_and_huge_weights():
     assert not got["R1"].any() and not got["c1"].any() and float(got["c2"]) == 300 and not got["R2"].any()
 
 
+@pytest.mark.parametrize("F", [18, 64, 128])
+@pytest.mark.parametrize("zero", ["weights", "features"])
+def test_hidden_layers_of_zero_add_nothing_to_dR2(F, zero):
+    """ssp(0) = 0: whatever the seeds, no term of dR2 is left."""
+    rng = np.random.default_rng(F)
+    codes, scales, _ = _stored(30_000, F, rng)
+    w = _weights(F, rng)
+    w["c1"][:] = 0
+    if zero == "weights":
+        w["R1"][:] = 0
+    else:
+        codes, scales = api.store_features(torch.zeros(30_000, F, device="cuda"))
+    off = list(range(0, 30_001, 30))
+    g = (rng.normal(size=1000) * np.exp(2 * rng.normal(size=1000))).astype(np.float32)
+    got = api.readout_gradients(codes, scales, _dev(off, torch.int32), _dw(w), _dev(g))
+    assert not got["R2"].any()
+
+
+@pytest.mark.parametrize("F", [18, 64, 128])
+def test_dR2_of_small_activations(F):
+    """p = c1 from 1e-6 to 2 in size: each term of dR2 to 2e-7 (the activation) and 3u (c1 log2 e and its product),
+    their sum to the u of at most 32 + 5 float32 additions before float64 takes over, and u at the end."""
+    rng = np.random.default_rng(F)
+    n, H = 50_000, F // 2
+    codes, scales, _ = _stored(n, F, rng)
+    w = _weights(F, rng)
+    w["R1"][:] = 0
+    w["c1"] = (np.geomspace(1e-6, 2.0, H) * np.where(np.arange(H) % 2, 1, -1)).astype(np.float32)
+    off = [0, 20_000, n]
+    g = np.array([1.0, 0.75], np.float32)
+    got = api.readout_gradients(codes, scales, _dev(off, torch.int32), _dw(w), _dev(g))["R2"].cpu().numpy()
+    p = w["c1"].astype(np.float64)
+    want = (20_000 + 0.75 * 30_000) * np.log1p(np.expm1(p) / 2.0)        # ssp(p) without cancellation
+    assert np.all(np.abs(got - want) <= (2e-7 + 41 * U) * np.abs(want))
+
+
 @pytest.mark.parametrize("F", [64, 128])
 @pytest.mark.parametrize("ex", [125, 126, 127])
 def test_weights_near_the_largest_finite(F, ex):
