@@ -370,7 +370,7 @@ SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, 
  *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
  * 0 <= n_atoms <= 0x7fff0000, 1 <= n_replicas <= 0x7ff00000.  A NaN or an infinity in R1 or c1 makes all
  * results NaN; hidden pre-activations, and a row's scale times the largest |R1|, are to stay below 2^126
- * in magnitude.  Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
+ * in magnitude.  A device-side wait that gives up makes all results NaN.  Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
 SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
                                                const int32_t *d_replica_offsets, const float *d_R1,
@@ -393,6 +393,15 @@ SCHNET_API schnet_status schnet_readout_gradients(const uint8_t *d_codes, const 
                                                   const float *d_grad_energy, float *d_dR1, float *d_dc1,
                                                   float *d_dR2, float *d_dc2, void *d_workspace, size_t ws_bytes,
                                                   void *cuda_stream);
+
+/* Test tap: what schnet_readout_energy does after its tensor-core kernel, on the caller's d_eps
+ * and chunk sums of 0; with given_up != 0 as if one of that kernel's bounded waits had given up:
+ * d_energy and d_eps become NaN.  1 <= n_atoms; arguments and errors otherwise as
+ * schnet_readout_energy, workspace as for 128 features. */
+SCHNET_API schnet_status schnet_test_readout_timeout(int32_t n_atoms, int32_t n_replicas,
+                                                     const int32_t *d_replica_offsets, int32_t given_up,
+                                                     float *d_energy, float *d_eps, void *d_workspace,
+                                                     size_t ws_bytes, void *cuda_stream);
 
 /* Device workspace bytes of schnet_readout_energy and schnet_readout_gradients on
  * the current device.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

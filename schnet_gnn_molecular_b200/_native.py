@@ -24,7 +24,7 @@ EXPORTED = ["schnet_workspace_bytes", "schnet_create", "schnet_build_neighbors",
             "schnet_get_neighbors", "schnet_get_atom_energies", "schnet_kernel_launches", "schnet_profile_steps",
             "schnet_build_neighbors_noalloc", "schnet_test_exp2", "schnet_test_timeout", "schnet_store_features",
             "schnet_get_features", "schnet_set_readout", "schnet_readout_energy", "schnet_readout_gradients",
-            "schnet_readout_workspace_bytes", "schnet_preference_loss", "schnet_preference_workspace_bytes"]
+            "schnet_readout_workspace_bytes", "schnet_test_readout_timeout", "schnet_preference_loss", "schnet_preference_workspace_bytes"]
 KERNEL_CLASSES = ["cfconv_fwd", "cfconv_bwd", "atomwise", "neighbors", "forces", "integrate", "reduce", "mask",
                   "cfconv_dh"]
 
@@ -102,6 +102,7 @@ def load() -> C.CDLL:
     L.schnet_readout_energy.argtypes = [vp, vp, i32, i32, i32] + [vp] * 8 + [sz, vp]
     L.schnet_readout_gradients.argtypes = [vp, vp, i32, i32, i32] + [vp] * 11 + [sz, vp]
     L.schnet_readout_workspace_bytes.argtypes = [i32, i32, szp]
+    L.schnet_test_readout_timeout.argtypes = [i32, i32, vp, i32, vp, vp, vp, sz, vp]
     L.schnet_preference_loss.argtypes = [vp, vp, i32, i32, vp, i64, C.c_double, C.c_double, vp, vp, vp, vp, vp, sz, vp]
     L.schnet_preference_workspace_bytes.argtypes = [i32, i64, szp]
     L.schnet_kernel_launches.argtypes = [vp]

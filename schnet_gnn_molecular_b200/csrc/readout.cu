@@ -518,7 +518,8 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
     }
 }
 
-// The replicas' energies: a warp each, or a CTA where replicas are long.
+// The replicas' energies: a warp each, or a CTA where replicas are long.  Where a CTA of the
+// kernel before gave up, every result is NaN, eps too (the rows it did not reach hold nothing).
 template <int TPR>
 __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
 {
@@ -535,6 +536,19 @@ __global__ void __launch_bounds__(256) k_readout_sums(ReadoutArgs a)
         for (int w = 0; w < 8; ++w) s += ws[w];
     }
     if (l == 0 && r < a.R) a.energy[r] = bad ? __int_as_float(0x7fffffff) : (float)s;
+    if (bad)
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < a.n; i += (long long)gridDim.x * 256)
+            a.eps[i] = __int_as_float(0x7fffffff);
+}
+
+// a warp per replica up to 4096 atoms a replica on average, else a CTA
+static schnet_status launch_sums(const ReadoutArgs& a, cudaStream_t s)
+{
+    const cudaError_t e = (int64_t)a.n > (int64_t)a.R * 4096
+                              ? launch_pdl(k_readout_sums<256>, a.R, 256, 0, s, a)
+                              : launch_pdl(k_readout_sums<32>, (a.R + 7) / 8, 256, 0, s, a);
+    if (e != cudaSuccess) return SCHNET_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -1164,11 +1178,29 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
         if (!code_map(a, &map) || !allow_smem((const void*)f, FWD_SMEM, dev, g_fwd_set[narrow])) return SCHNET_ERR_CUDA;
         f<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
     }
-    // a warp per replica up to 4096 atoms a replica on average, else a CTA
-    cudaError_t e = (int64_t)a.n > (int64_t)a.R * 4096 ? launch_pdl(k_readout_sums<256>, a.R, 256, 0, s, a)
-                                                      : launch_pdl(k_readout_sums<32>, (a.R + 7) / 8, 256, 0, s, a);
-    if (e != cudaSuccess) return SCHNET_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+    return launch_sums(a, s);
+}
+
+extern "C" schnet_status schnet_test_readout_timeout(int32_t n_atoms, int32_t n_replicas,
+                                                     const int32_t* d_replica_offsets, int32_t given_up,
+                                                     float* d_energy, float* d_eps, void* d_workspace,
+                                                     size_t ws_bytes, void* cuda_stream)
+{
+    size_t need = 0;
+    if (schnet_readout_workspace_bytes(n_atoms, FP, &need) != SCHNET_OK || n_atoms < 1 || n_replicas < 1 ||
+        n_replicas > MAX_REPLICAS || !d_replica_offsets || !d_energy || !d_eps || !d_workspace ||
+        ((uintptr_t)d_workspace & 255) || ws_bytes < need)
+        return SCHNET_ERR_INVALID_ARG;
+    ReadoutArgs a{};
+    a.n = n_atoms; a.R = n_replicas; a.off = d_replica_offsets; a.energy = d_energy; a.eps = d_eps;
+    a.ncta = std::min((n_atoms + 127) / 128, MAX_SM);
+    a.status = (uint32_t*)d_workspace;
+    a.csum = (double*)(a.status + MAX_SM);
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    if (cudaMemsetAsync(d_workspace, 0, need, s) != cudaSuccess ||
+        (given_up && cudaMemsetAsync(a.status + a.ncta - 1, 1, sizeof(uint32_t), s) != cudaSuccess))
+        return SCHNET_ERR_CUDA;
+    return launch_sums(a, s);
 }
 
 extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const uint8_t* d_scales, int32_t n_atoms,

@@ -6,6 +6,7 @@ products of them with R1, carried to 2^-22 or better and accumulated in fp32, on
 nearest (up to 2u a step, at most 2 F / 16 + F steps): |dp| <= (2 F + 16) 2u (|x| |R1| + |c1|) =: b.  ssp and sigma
 have slopes of at most 1 and 1/4 and are formed from a base-2 exponential and logarithm good to 2^-22, so to
 2^-20 (1 + |p|).  Sums over atoms are chains of at most 512 roundings (longer ones are cut into partial sums)."""
+import ctypes as C
 import os
 import subprocess
 import sys
@@ -335,6 +336,23 @@ LAYOUTS["tiles"] = (500_009, [0, *range(11, 500_000, 131), 500_009])
 def test_many_tiles(F):
     test_readout_energy("tiles", F)
     test_readout_gradients("tiles", F)
+
+
+@pytest.mark.parametrize("n,R", [(1, 1), (5000, 3), (100_000, 3), (300, 900)])
+def test_a_wait_that_gives_up_makes_every_result_nan(n, R):
+    lib = nat.load()
+    need = C.c_size_t(0)
+    assert lib.schnet_readout_workspace_bytes(n, 128, C.byref(need)) == 0
+    off = _dev(np.linspace(0, n, R + 1).astype(np.int32))
+    ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    stream = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    p = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+    for given_up in (0, 1):
+        E, eps = torch.ones(R, device="cuda"), torch.ones(n, device="cuda")
+        assert lib.schnet_test_readout_timeout(n, R, p(off), given_up, p(E), p(eps), p(ws), need.value, stream) == 0
+        assert torch.isnan(E).all() == bool(given_up) and torch.isnan(eps).all() == bool(given_up)
+        if not given_up:
+            assert torch.isfinite(E).all() and torch.equal(eps, torch.ones_like(eps))
 
 
 def test_same_inputs_same_bits():

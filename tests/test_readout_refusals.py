@@ -81,6 +81,14 @@ def test_preference_refusals(lib):
     assert lib.schnet_preference_workspace_bytes(1, 1, None) == 1
 
 
+def test_timeout_tap_refusals(lib):
+    def call(n=8, R=2, off=P, e=P, eps=P, ws=P, size=1 << 40):
+        return lib.schnet_test_readout_timeout(n, R, off, 1, e, eps, ws, size, None)
+    for bad in (dict(n=0), dict(n=-1), dict(R=0), dict(R=MAX_REPLICAS + 1), dict(off=None), dict(e=None), dict(eps=None),
+                dict(ws=None), dict(ws=C.c_void_p(4100)), dict(size=64)):
+        assert call(**bad) == 1, bad
+
+
 def test_context_calls_refuse_null(lib):
     assert lib.schnet_get_features(None, P, P) == 1
     assert lib.schnet_set_readout(None, P, P, P, 0.0) == 1
