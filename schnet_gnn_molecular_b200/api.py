@@ -216,8 +216,8 @@ def store_features(x: torch.Tensor):
 
 
 def readout_energy(codes, scales, replica_offsets, readout):
-    """(energy [R], eps [n]) float32: readout energies from stored features.  replica_offsets int32 [R + 1] on the
-    device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
+    """(energy [R], eps [n]) float32: readout energies from stored features (codes and scales of store_features, or
+    their bytes as uint8).  replica_offsets int32 [R + 1] on the device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
     return _checked(nat.binding().readout_energy(codes, scales, replica_offsets, readout["R1"], readout["c1"],
                                                  readout["R2"], readout["c2"]), "readout_energy")
 

@@ -29,18 +29,25 @@ const Tensor& tensor(PyObject* o, const char* name)
 
 [[noreturn]] void refuse(const std::string& what) { throw c10::ValueError({__func__, __FILE__, __LINE__}, what); }
 
-// t: a contiguous tensor of that shape on device dev; dtype Undefined: any of one byte
+// t: a contiguous tensor of that shape on device dev
 void check(const char* name, const Tensor& t, int dev, ScalarType dtype, std::initializer_list<int64_t> shape)
 {
-    const bool type = dtype == ScalarType::Undefined ? t.element_size() == 1 : t.scalar_type() == dtype;
-    if (t.is_cuda() && t.get_device() == dev && type && t.is_contiguous() &&
+    if (t.is_cuda() && t.get_device() == dev && t.scalar_type() == dtype && t.is_contiguous() &&
         t.sizes() == at::IntArrayRef(shape.begin(), shape.size()))
         return;
     std::string want;
     for (int64_t s : shape) want += (want.empty() ? "" : ", ") + std::to_string(s);
-    refuse(std::string(name) + " must be a contiguous tensor of " +
-           (dtype == ScalarType::Undefined ? "bytes" : c10::toString(dtype)) + " and shape (" + want + ") on device " +
-           std::to_string(dev));
+    refuse(std::string(name) + " must be a contiguous tensor of " + c10::toString(dtype) + " and shape (" + want +
+           ") on device " + std::to_string(dev));
+}
+
+// the type of stored codes or scales: their own, or plain bytes; any other 8-bit type means other values
+ScalarType stored_type(const char* name, const Tensor& t, ScalarType own)
+{
+    const ScalarType type = t.scalar_type();
+    if (type != own && type != ScalarType::Byte)
+        refuse(std::string(name) + " must be " + c10::toString(own) + " or Byte, not " + c10::toString(type));
+    return type;
 }
 
 Tensor make(int dev, ScalarType dtype, std::initializer_list<int64_t> shape)
@@ -108,6 +115,8 @@ struct ReadoutCall {
         : codes(tensor(a[0], "codes")), scales(tensor(a[1], "scales")), off(tensor(a[2], "replica_offsets")),
           R1(tensor(a[3], "R1")), c1(tensor(a[4], "c1")), R2(tensor(a[5], "R2")), c2(tensor(a[6], "c2"))
     {
+        const ScalarType code_type = stored_type("codes", codes, ScalarType::Float8_e4m3fn);
+        const ScalarType scale_type = stored_type("scales", scales, ScalarType::Float8_e8m0fnu);
         if (!codes.is_cuda() || codes.dim() != 2 || R1.dim() != 2 || off.dim() != 1 || c2.numel() != 1)
             refuse("codes [n, width], R1 [F, F / 2], c2 [1] and replica_offsets [R + 1] must be CUDA tensors");
         dev = codes.get_device();
@@ -117,8 +126,8 @@ struct ReadoutCall {
         R = off.size(0) - 1;
         if (F != 2 * H || R < 1 || n >= INT32_MAX || R >= INT32_MAX)
             refuse("R1 must be [F, F / 2]; replica_offsets [R + 1] with R >= 1; fewer than 2^31 atoms and replicas");
-        check("codes", codes, dev, ScalarType::Undefined, {n, width(F)});
-        check("scales", scales, dev, ScalarType::Undefined, {n});
+        check("codes", codes, dev, code_type, {n, width(F)});
+        check("scales", scales, dev, scale_type, {n});
         check("replica_offsets", off, dev, ScalarType::Int, {R + 1});
         check("R1", R1, dev, ScalarType::Float, {F, H});
         check("c1", c1, dev, ScalarType::Float, {H});

@@ -105,3 +105,21 @@ def test_binding_refuses_host_tensors(lib):
         api.readout_energy(codes, scales, off, w)
     with pytest.raises(ValueError):
         api.preference_loss(torch.zeros(4), torch.zeros(1, 2, dtype=torch.int32), kT=1.0)
+
+
+def test_binding_refuses_other_8_bit_types(lib):
+    """Their bytes are not e4m3 codes and e8m0 scales; plain bytes are taken as such."""
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    w = {"R1": torch.zeros(64, 32), "c1": torch.zeros(32), "R2": torch.zeros(32), "c2": torch.zeros(1)}
+    off, g = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(1)
+    calls = (lambda c, s: api.readout_energy(c, s, off, w), lambda c, s: api.readout_gradients(c, s, off, w, g))
+    for call in calls:
+        for t in (torch.int8, torch.bool, torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e8m0fnu):
+            with pytest.raises(ValueError, match="codes must be Float8_e4m3fn or Byte"):
+                call(codes.view(t), scales)
+        for t in (torch.int8, torch.bool, torch.float8_e4m3fn):
+            with pytest.raises(ValueError, match="scales must be Float8_e8m0fnu or Byte"):
+                call(codes, scales.view(t))
+        for c, s in ((codes, scales), (codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu))):
+            with pytest.raises(ValueError, match="CUDA"):
+                call(c, s)
