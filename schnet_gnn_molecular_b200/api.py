@@ -194,7 +194,9 @@ class SchNet:
 
 
 # ----------------------------------------------------------------------
-# readout tuning: tensors in, tensors out, on the current stream of their device
+# readout tuning: tensors in, tensors out, on the current stream of their device.  The calls form no autograd
+# graph (the gradients are calls of their own), so a tensor that requires grad is refused with grad mode on: pass
+# it detached, or call under torch.no_grad().
 # ----------------------------------------------------------------------
 def feature_width(F: int) -> int:
     """Columns of a row of stored features: F rounded up to a multiple of 16."""
@@ -217,7 +219,8 @@ def store_features(x: torch.Tensor):
 
 def readout_energy(codes, scales, replica_offsets, readout):
     """(energy [R], eps [n]) float32: readout energies from stored features (codes and scales of store_features, or
-    their bytes as uint8).  replica_offsets int32 [R + 1] on the device; readout: {"R1" [F, F/2], "c1", "R2" [F/2], "c2" [1]} float32 device tensors."""
+    their bytes as uint8).  replica_offsets int32 [R + 1] on the device; readout: {"R1" [F, F/2], "c1", "R2" [F/2],
+    "c2" [1]} float32 device tensors."""
     return _checked(nat.binding().readout_energy(codes, scales, replica_offsets, readout["R1"], readout["c1"],
                                                  readout["R2"], readout["c2"]), "readout_energy")
 

@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -21,13 +22,18 @@ namespace {
 using at::ScalarType;
 using at::Tensor;
 
+[[noreturn]] void refuse(const std::string& what) { throw c10::ValueError({__func__, __FILE__, __LINE__}, what); }
+
+// These calls record nothing for autograd: an argument whose gradient would get lost is refused.
 const Tensor& tensor(PyObject* o, const char* name)
 {
     if (!THPVariable_Check(o)) throw torch::TypeError(std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse(std::string(name) + " requires grad, and this call forms no autograd graph: detach it, or call under "
+                                   "torch.no_grad()");
+    return t;
 }
-
-[[noreturn]] void refuse(const std::string& what) { throw c10::ValueError({__func__, __FILE__, __LINE__}, what); }
 
 // t: a contiguous tensor of that shape on device dev
 void check(const char* name, const Tensor& t, int dev, ScalarType dtype, std::initializer_list<int64_t> shape)
@@ -159,8 +165,8 @@ PyObject* readout_gradients(PyObject*, PyObject* const* args, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     if (!arity(n_args, 8)) return nullptr;
-    const ReadoutCall c(args);
     const Tensor& g = tensor(args[7], "grad_energy");
+    const ReadoutCall c(args);
     check("grad_energy", g, c.dev, ScalarType::Float, {c.R});
     size_t size = 0;
     schnet_status st = schnet_readout_workspace_bytes((int32_t)c.n, (int32_t)c.F, &size);
@@ -183,6 +189,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n_args)
     HANDLE_TH_ERRORS
     if (!arity(n_args, 6)) return nullptr;
     const Tensor &energy = tensor(args[0], "energy"), &pairs = tensor(args[1], "pairs");
+    const Tensor* ref = args[2] == Py_None ? nullptr : &tensor(args[2], "reference");
     const ScalarType t = energy.scalar_type();
     if (!energy.is_cuda() || energy.dim() != 1 || energy.size(0) < 1 || !energy.is_contiguous() ||
         (t != ScalarType::Float && t != ScalarType::Double))
@@ -193,10 +200,9 @@ PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n_args)
     if (R >= INT32_MAX || P >= INT32_MAX) refuse("fewer than 2^31 replicas and pairs");
     check("pairs", pairs, dev, ScalarType::Int, {P, 2});
     const void* reference = nullptr;
-    if (args[2] != Py_None) {
-        const Tensor& r = tensor(args[2], "reference");
-        check("reference", r, dev, t, {R});
-        reference = r.data_ptr();
+    if (ref) {
+        check("reference", *ref, dev, t, {R});
+        reference = ref->data_ptr();
     }
     uint32_t* flags = nullptr;
     if (args[3] != Py_None) {

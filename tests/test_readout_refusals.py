@@ -123,3 +123,26 @@ def test_binding_refuses_other_8_bit_types(lib):
         for c, s in ((codes, scales), (codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu))):
             with pytest.raises(ValueError, match="CUDA"):
                 call(c, s)
+
+
+def test_binding_refuses_what_autograd_would_lose(lib):
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    w = {"R1": torch.zeros(64, 32), "c1": torch.zeros(32), "R2": torch.zeros(32), "c2": torch.zeros(1)}
+    off, g = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(1)
+    E, pairs = torch.zeros(4), torch.zeros(1, 2, dtype=torch.int32)
+    calls = [("x", lambda t: api.store_features(t), torch.zeros(4, 64)),
+             ("grad_energy", lambda t: api.readout_gradients(codes, scales, off, w, t), g),
+             ("energy", lambda t: api.preference_loss(t, pairs, kT=1.0), E),
+             ("reference", lambda t: api.preference_loss(E, pairs, kT=1.0, reference=t), E)]
+    for k in w:
+        calls.append((k, lambda t, k=k: api.readout_energy(codes, scales, off, dict(w, **{k: t})), w[k]))
+        calls.append((k, lambda t, k=k: api.readout_gradients(codes, scales, off, dict(w, **{k: t}), g), w[k]))
+    for name, call, t in calls:
+        leaf = t.clone().requires_grad_()
+        for value in (leaf, leaf * 2):
+            with pytest.raises(ValueError, match=f"{name} requires grad"):
+                call(value)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(value)
+            with pytest.raises(ValueError, match="CUDA"):
+                call(value.detach())
