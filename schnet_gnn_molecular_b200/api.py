@@ -155,12 +155,18 @@ class SchNet:
 
     def features(self):
         """(codes, scales): the trunk's output features of the last evaluation in 8 bits, as store_features
-        gives them, in the caller's atom order.  Made on the stream the model was created with."""
+        gives them, in the caller's atom order.  Made on the stream the model was created with; the current
+        stream, where the readout calls will read them, waits for it."""
         W = feature_width(self.cfg.n_features)
         with torch.cuda.stream(self.stream):
             codes = torch.empty((self.n_atoms, W), dtype=torch.float8_e4m3fn, device=self.device)
             scales = torch.empty(self.n_atoms, dtype=torch.float8_e8m0fnu, device=self.device)
-        self._check(self.lib.schnet_get_features(self.ctx, _ptr(codes), _ptr(scales)), "features")
+            self._check(self.lib.schnet_get_features(self.ctx, _ptr(codes), _ptr(scales)), "features")
+        reader = torch.cuda.current_stream(self.device)
+        if reader != self.stream:
+            reader.wait_stream(self.stream)
+            codes.record_stream(reader)
+            scales.record_stream(reader)
         return codes, scales
 
     def set_readout(self, readout):

@@ -679,6 +679,32 @@ def test_a_tuning_loop_over_frames():
     model.set_readout(readout)
 
 
+def test_features_are_ready_on_the_current_stream():
+    """The model lives on one stream, which is busy; the features are read on another at once."""
+    w = W4
+    own, reader = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(own):
+        model = api.from_workload(w, workloads.weights(w), device="cuda")
+        pos, types = _dev(workloads.positions(w)), _dev(workloads.types(w), torch.int32)
+        model.build_neighbors(pos)
+        model.energy_forces(pos, types, forces=False)
+        want = [t.view(torch.uint8).clone() for t in model.features()]
+        # the memory that the next features will be given holds something else
+        for t in [torch.full_like(t, 0x55) for t in want]:
+            del t
+        own.synchronize()
+        torch.cuda._sleep(100_000_000)            # some 50 ms
+    with torch.cuda.stream(reader):
+        codes, scales = model.features()
+        got = [codes.view(torch.uint8).clone(), scales.view(torch.uint8).clone()]
+        del codes, scales                         # (their memory stays theirs until the copies are made)
+    with torch.cuda.stream(own):
+        for t in [torch.full_like(t, 0x55) for t in want]:
+            del t
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_set_readout_refusals():
     w = workloads.TINY
     m = api.from_workload(w, workloads.weights(w))
