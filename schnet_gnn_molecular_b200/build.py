@@ -7,6 +7,7 @@ The library exports the C ABI declared in ``include/schnet.h``.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 
@@ -18,7 +19,8 @@ SOURCES = ["api.cu", "neighbors.cu", "cfconv.cu", "atomwise.cu", "integrate.cu",
            "preference.cu"]
 HEADERS = ["common.cuh", "internal.h", os.path.join("..", "..", "include", "schnet.h")]
 
-NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CUDA_DEFAULT = "/usr/local/cuda"
+NVCC = os.environ.get("NVCC", os.path.join(CUDA_DEFAULT, "bin", "nvcc"))
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "-ftz=true",
          "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -35,17 +37,26 @@ def _stale(target: str, sources: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def cuda_include() -> str:
+    """The folder of CUDA's headers: nvcc's own, whether NVCC is a path, a link or a name on PATH; else CUDA_HOME's."""
+    nvcc = shutil.which(NVCC)
+    homes = [os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))] if nvcc else []
+    for home in [*homes, os.environ.get("CUDA_HOME"), CUDA_DEFAULT]:
+        if home and os.path.exists(os.path.join(home, "include", "cuda_runtime_api.h")):
+            return os.path.join(home, "include")
+    raise RuntimeError(f"no cuda_runtime_api.h beside {NVCC}, in CUDA_HOME or in {CUDA_DEFAULT}")
+
+
 def _build_binding(verbose: bool) -> None:
     import sysconfig
 
     import torch
     top = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in (os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
-                         os.path.join(cuda, "include"), sysconfig.get_paths()["include"]) for x in ("-isystem", d)],
+                         cuda_include(), sysconfig.get_paths()["include"]) for x in ("-isystem", d)],
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", HERE, "-l:" + os.path.basename(LIB),
            "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
            "-Wl,-rpath,$ORIGIN"]
