@@ -6,6 +6,7 @@ The library exports the C ABI declared in ``include/schnet.h``.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -35,6 +36,20 @@ def _stale(target: str, sources: list[str]) -> bool:
     t = os.path.getmtime(target)
     deps = [os.path.join(CSRC, s) for s in sources] + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def built_for() -> str:
+    """What a binding fits beside its sources: this PyTorch and this interpreter."""
+    return f"torch {importlib.metadata.version('torch')} {sys.implementation.cache_tag}"
+
+
+def _other_torch() -> bool:
+    """Whether the binding was built for another PyTorch or interpreter (its note, beside it, says which)."""
+    try:
+        with open(BINDING + ".txt") as f:
+            return f.read() != built_for()
+    except OSError:
+        return True
 
 
 def cuda_include() -> str:
@@ -69,8 +84,10 @@ def _build_binding(verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     if force or _stale(LIB, SOURCES + HEADERS):
         _build_library(verbose, extra)
-    if force or _stale(BINDING, BINDING_SOURCES):
+    if force or _stale(BINDING, BINDING_SOURCES) or _other_torch():
         _build_binding(verbose)
+        with open(BINDING + ".txt", "w") as f:
+            f.write(built_for())
     return LIB
 
 

@@ -29,3 +29,27 @@ def test_missing_cuda_headers_are_reported(monkeypatch, tmp_path):
     monkeypatch.setenv("CUDA_HOME", str(tmp_path))
     with pytest.raises(RuntimeError, match="cuda_runtime_api.h"):
         build.cuda_include()
+
+
+@pytest.fixture
+def calls(monkeypatch, tmp_path):
+    """What build() would do, with a library and a binding newer than their sources."""
+    done = []
+    for name, attr in (("lib.so", "LIB"), ("binding.so", "BINDING")):
+        (tmp_path / name).write_bytes(b"")
+        monkeypatch.setattr(build, attr, str(tmp_path / name))
+    monkeypatch.setattr(build, "_build_library", lambda verbose, extra: done.append("library"))
+    monkeypatch.setattr(build, "_build_binding", lambda verbose: done.append("binding"))
+    return done
+
+
+def test_a_binding_of_another_pytorch_is_stale(monkeypatch, calls):
+    build.build()
+    assert calls == ["binding"]                   # built for nobody knows what
+    build.build()
+    assert calls == ["binding"]
+    monkeypatch.setattr(build, "built_for", lambda: "torch 0.1 cpython-27")
+    build.build()
+    assert calls == ["binding", "binding"]
+    build.build()
+    assert calls == ["binding", "binding"]
