@@ -1,8 +1,9 @@
 """Build the sm_100a shared library ``libschnet_b200.so`` in-tree with nvcc, and
 the Python binding of its readout-tuning calls, ``_binding.so``, with g++.
 
-Usage: ``python -m schnet_gnn_molecular_b200.build [--force] [--verbose]``.
-The library exports the C ABI declared in ``include/schnet.h``.
+Usage: ``python -m schnet_gnn_molecular_b200.build [--force] [--verbose] [--library-only]``.
+The library exports the C ABI declared in ``include/schnet.h``; building it alone (``--library-only``, or without
+PyTorch installed) needs nvcc only.
 """
 from __future__ import annotations
 
@@ -81,9 +82,19 @@ def _build_binding(verbose: bool) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+def _have_torch() -> bool:
+    try:
+        return bool(built_for())
+    except importlib.metadata.PackageNotFoundError:
+        return False
+
+
+def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, binding: bool = True) -> str:
+    """binding = False, or no PyTorch: the library alone, which is all that a user of the C ABI needs."""
     if force or _stale(LIB, SOURCES + HEADERS):
         _build_library(verbose, extra)
+    if not binding or not _have_torch():
+        return LIB
     if force or _stale(BINDING, BINDING_SOURCES) or _other_torch():
         _build_binding(verbose)
         with open(BINDING + ".txt", "w") as f:
@@ -103,4 +114,5 @@ def _build_library(verbose: bool, extra: list[str] | None) -> None:
 
 if __name__ == "__main__":
     extra = ["-Xptxas", "-v"] if "--ptxas" in sys.argv else None
-    print(build(force="--force" in sys.argv, verbose="--verbose" in sys.argv or extra is not None, extra=extra))
+    print(build(force="--force" in sys.argv, verbose="--verbose" in sys.argv or extra is not None, extra=extra,
+                binding="--library-only" not in sys.argv))

@@ -1,4 +1,5 @@
 """The build's own decisions, without building: where CUDA's headers are."""
+import importlib.metadata
 import os
 import shutil
 
@@ -53,3 +54,14 @@ def test_a_binding_of_another_pytorch_is_stale(monkeypatch, calls):
     assert calls == ["binding", "binding"]
     build.build()
     assert calls == ["binding", "binding"]
+
+
+def test_the_library_alone_needs_no_pytorch(monkeypatch, calls):
+    def gone():
+        raise importlib.metadata.PackageNotFoundError("torch")
+    build.build(binding=False)
+    assert calls == []
+    monkeypatch.setattr(build, "built_for", gone)
+    build.build()                                 # no PyTorch: nothing to bind to
+    build.build(force=True)
+    assert calls == ["library"]
