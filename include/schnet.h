@@ -427,7 +427,7 @@ SCHNET_API schnet_status schnet_readout_workspace_bytes(int32_t n_atoms, int32_t
  * as 64-bit integers, which add up to the same value in any order; with b the bits of
  * n_pairs, a slope is kept to 2^-25 of itself down to 2^(2b - 76) and to 2^(2b - 101)
  * below that.
- * kT > 0; 0 <= smoothing <= 1; 1 <= n_replicas <= 0x7ff00000; 0 <= n_pairs < 2^31.
+ * kT > 0, 1 / kT finite; 0 <= smoothing <= 1; 1 <= n_replicas <= 0x7ff00000; 0 <= n_pairs < 2^31.
  * Errors: INVALID_ARG, CUDA. */
 SCHNET_API schnet_status schnet_preference_loss(const void *d_energy, const void *d_reference, int32_t dtype,
                                                 int32_t n_replicas, const int32_t *d_pairs, int64_t n_pairs,

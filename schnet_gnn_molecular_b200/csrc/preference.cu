@@ -278,7 +278,7 @@ extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void
 {
     size_t need = 0;
     if (!d_energy || !d_loss || !d_grad_energy || !d_workspace || ((uintptr_t)d_workspace & 255) ||
-        (dtype != SCHNET_FLOAT32 && dtype != SCHNET_FLOAT64) || !(kT > 0.0) || !std::isfinite(kT) ||
+        (dtype != SCHNET_FLOAT32 && dtype != SCHNET_FLOAT64) || !(kT > 0.0) || !std::isfinite(kT) || !std::isfinite(1.0 / kT) ||
         !(smoothing >= 0.0 && smoothing <= 1.0) ||
         schnet_preference_workspace_bytes(n_replicas, n_pairs, &need) != SCHNET_OK || ws_bytes < need ||
         (n_pairs > 0 && !d_pairs) || ((uintptr_t)d_pairs & 7))

@@ -81,6 +81,12 @@ def test_preference_refusals(lib):
     assert lib.schnet_preference_workspace_bytes(1, 1, None) == 1
 
 
+def test_kT_whose_reciprocal_is_infinite(lib):
+    """Margins of 0 would be 0 times infinity."""
+    for kT in (5e-324, 5.5e-309):
+        assert lib.schnet_preference_loss(P, None, 0, 16, P, 9, kT, 0.0, P, None, P, None, P, 1 << 40, None) == 1
+
+
 def test_timeout_tap_refusals(lib):
     def call(n=8, R=2, off=P, e=P, eps=P, ws=P, size=1 << 40):
         return lib.schnet_test_readout_timeout(n, R, off, 1, e, eps, ws, size, None)
