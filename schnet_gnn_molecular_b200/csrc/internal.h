@@ -144,6 +144,14 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The status of a call without a context whose last launch returned e.  An error of its own does
+// not stay pending on the thread, where the next call would take it for one from before.
+inline schnet_status enqueued(cudaError_t e)
+{
+    const cudaError_t last = cudaGetLastError();
+    return e == cudaSuccess && last == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+}
+
 }  // namespace schnet
 
 struct schnet_ctx {

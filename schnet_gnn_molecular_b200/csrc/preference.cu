@@ -307,14 +307,14 @@ extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void
         const size_t smem = (size_t)n_replicas * 24;
         if (f64) k_pref_small<double><<<1, SMALL_T, smem, s>>>(a);
         else k_pref_small<float><<<1, SMALL_T, smem, s>>>(a);
-        return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+        return enqueued(cudaSuccess);
     }
     const int g1 = (int)std::max<int64_t>(1, std::min<int64_t>((n_pairs + PT - 1) / PT, PREF_MAX_CTA));
     const int g2 = std::min((n_replicas + PT - 1) / PT, PREF_MAX_CTA);
     if (f64) k_pref_gaps<double><<<g2, PT, 0, s>>>(a);
     else k_pref_gaps<float><<<g2, PT, 0, s>>>(a);
-    if (launch_pdl(k_pref_pairs, g1, PT, 0, s, a) != cudaSuccess ||
-        launch_pdl(k_pref_finish, g2, PT, 0, s, a, g1) != cudaSuccess)
-        return SCHNET_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+    cudaError_t e = cudaPeekAtLastError();
+    if (e == cudaSuccess) e = launch_pdl(k_pref_pairs, g1, PT, 0, s, a);
+    if (e == cudaSuccess) e = launch_pdl(k_pref_finish, g2, PT, 0, s, a, g1);
+    return enqueued(e);
 }

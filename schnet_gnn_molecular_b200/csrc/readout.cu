@@ -547,8 +547,7 @@ static schnet_status launch_sums(const ReadoutArgs& a, cudaStream_t s)
     const cudaError_t e = (int64_t)a.n > (int64_t)a.R * 4096
                               ? launch_pdl(k_readout_sums<256>, a.R, 256, 0, s, a)
                               : launch_pdl(k_readout_sums<32>, (a.R + 7) / 8, 256, 0, s, a);
-    if (e != cudaSuccess) return SCHNET_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+    return enqueued(e);
 }
 
 // ---------------------------------------------------------------------------
@@ -1071,12 +1070,12 @@ static int sm_count(int dev)
 }
 
 // more than 48 KB of shared memory for a kernel, once per device
-static bool allow_smem(const void* kernel, uint32_t bytes, int dev, std::atomic<uint64_t>& set)
+static cudaError_t allow_smem(const void* kernel, uint32_t bytes, int dev, std::atomic<uint64_t>& set)
 {
-    if (dev < 64 && (set.load() >> dev & 1)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-    if (dev < 64) set.fetch_or((uint64_t)1 << dev);
-    return true;
+    if (dev < 64 && (set.load() >> dev & 1)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) set.fetch_or((uint64_t)1 << dev);
+    return e;
 }
 static std::atomic<uint64_t> g_fwd_set[2], g_grad_set[2];        // [narrow]
 
@@ -1167,7 +1166,7 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
     a.eps = d_eps;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return SCHNET_ERR_CUDA;
+    if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return enqueued(e);
     a.ncta = std::min((a.n + 127) / 128, sm_count(dev));
     a.status = (uint32_t*)d_workspace;
     a.csum = (double*)(a.status + MAX_SM);
@@ -1175,8 +1174,13 @@ extern "C" schnet_status schnet_readout_energy(const uint8_t* d_codes, const uin
         CUtensorMap map;
         const bool narrow = a.F <= 64;
         const auto f = narrow ? k_readout_eps<64> : k_readout_eps<128>;
-        if (!code_map(a, &map) || !allow_smem((const void*)f, FWD_SMEM, dev, g_fwd_set[narrow])) return SCHNET_ERR_CUDA;
-        f<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
+        if (!code_map(a, &map)) return SCHNET_ERR_CUDA;
+        cudaError_t e = allow_smem((const void*)f, FWD_SMEM, dev, g_fwd_set[narrow]);
+        if (e == cudaSuccess) {
+            f<<<a.ncta, FWD_THREADS, FWD_SMEM, s>>>(map, a);
+            e = cudaPeekAtLastError();
+        }
+        if (e != cudaSuccess) return enqueued(e);
     }
     return launch_sums(a, s);
 }
@@ -1197,10 +1201,9 @@ extern "C" schnet_status schnet_test_readout_timeout(int32_t n_atoms, int32_t n_
     a.status = (uint32_t*)d_workspace;
     a.csum = (double*)(a.status + MAX_SM);
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    if (cudaMemsetAsync(d_workspace, 0, need, s) != cudaSuccess ||
-        (given_up && cudaMemsetAsync(a.status + a.ncta - 1, 1, sizeof(uint32_t), s) != cudaSuccess))
-        return SCHNET_ERR_CUDA;
-    return launch_sums(a, s);
+    cudaError_t e = cudaMemsetAsync(d_workspace, 0, need, s);
+    if (e == cudaSuccess && given_up) e = cudaMemsetAsync(a.status + a.ncta - 1, 1, sizeof(uint32_t), s);
+    return e == cudaSuccess ? launch_sums(a, s) : enqueued(e);
 }
 
 extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const uint8_t* d_scales, int32_t n_atoms,
@@ -1220,7 +1223,7 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
     a.gE = d_grad_energy;
     a.dR1 = d_dR1; a.dc1 = d_dc1; a.dR2 = d_dR2; a.dc2 = d_dc2;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return SCHNET_ERR_CUDA;
+    if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return enqueued(e);
     a.ncta = std::min((a.n + 127) / 128, sm_count(dev));
     a.status = (uint32_t*)d_workspace;
     a.nseed = a.n > 0 ? std::min(std::max((a.n + SEED_ATOMS - 1) / SEED_ATOMS, (a.R + 1023) / 1024), MAX_SEED) : 0;
@@ -1233,11 +1236,14 @@ extern "C" schnet_status schnet_readout_gradients(const uint8_t* d_codes, const 
         CUtensorMap map;
         const bool narrow = a.F <= 64;
         const auto f = narrow ? k_readout_grad<64> : k_readout_grad<128>;
-        if (!code_map(a, &map) || !allow_smem((const void*)f, GRAD_SMEM, dev, g_grad_set[narrow]))
-            return SCHNET_ERR_CUDA;
-        k_readout_seeds<<<a.nseed, 256, 0, s>>>(a);
-        if (launch_pdl(f, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a) != cudaSuccess) return SCHNET_ERR_CUDA;
+        if (!code_map(a, &map)) return SCHNET_ERR_CUDA;
+        cudaError_t e = allow_smem((const void*)f, GRAD_SMEM, dev, g_grad_set[narrow]);
+        if (e == cudaSuccess) {
+            k_readout_seeds<<<a.nseed, 256, 0, s>>>(a);
+            e = cudaPeekAtLastError();
+        }
+        if (e == cudaSuccess) e = launch_pdl(f, a.ncta, GRAD_THREADS, GRAD_SMEM, s, map, a);
+        if (e != cudaSuccess) return enqueued(e);
     }
-    if (launch_pdl(k_readout_grad_sum, 4 * a.H + 5, 256, 0, s, a) != cudaSuccess) return SCHNET_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SCHNET_OK : SCHNET_ERR_CUDA;
+    return enqueued(launch_pdl(k_readout_grad_sum, 4 * a.H + 5, 256, 0, s, a));
 }

@@ -648,6 +648,56 @@ assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=240)
 
 
+def test_a_call_that_fails_leaves_no_error_behind():
+    """Calls into a capture that has already failed report it, and the next call on a sound stream works."""
+    code = """
+import ctypes as C
+import torch
+from schnet_gnn_molecular_b200 import _native as nat
+from schnet_gnn_molecular_b200 import api
+lib = nat.load()
+x = torch.arange(300 * 64, device="cuda").reshape(300, 64).float().cos()
+off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+w = {"R1": x[:64, :32].contiguous(), "c1": x[0, :32].clone(), "R2": x[1, :32].clone(), "c2": x[2, :1].clone()}
+g = torch.ones(2, device="cuda")
+E5, pairs = torch.arange(5000, device="cuda").float(), torch.randint(0, 5000, (3000, 2), device="cuda").int()
+codes, scales = api.store_features(x)
+want = [api.readout_energy(codes, scales, off, w)[0], api.readout_gradients(codes, scales, off, w, g)["R1"],
+        api.preference_loss(E5, pairs, kT=1.0)[2]]
+E, eps, dR1, dc1, dR2, dc2 = (torch.zeros(n, device="cuda") for n in (2, 300, 64 * 32, 32, 32, 1))
+loss, dE = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(5000, device="cuda")
+ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+p = lambda t: C.c_void_p(t.data_ptr())
+def calls(stream):
+    s, n = C.c_void_p(stream.cuda_stream), ws.numel()
+    head = (p(codes), p(scales), 300, 64, 2, p(off), p(w["R1"]), p(w["c1"]), p(w["R2"]), p(w["c2"]))
+    return (lib.schnet_readout_energy(*head, p(E), p(eps), p(ws), n, s),
+            lib.schnet_readout_gradients(*head, p(g), p(dR1), p(dc1), p(dR2), p(dc2), p(ws), n, s),
+            lib.schnet_preference_loss(p(E5), None, 0, 5000, p(pairs), 3000, 1.0, 0.0, p(loss), None, p(dE), None,
+                                       p(ws), n, s))
+main = torch.cuda.current_stream()
+torch.cuda.synchronize()
+for first in range(3):
+    try:
+        side = torch.cuda.Stream()
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            try:
+                torch.cuda.synchronize()          # not allowed here: the capture is lost
+            except RuntimeError:
+                pass
+            status = calls(side)[first]
+    except RuntimeError:
+        pass
+    assert status == 2, status
+    torch.cuda.set_stream(main)
+    assert calls(main) == (0, 0, 0), first
+    torch.cuda.synchronize()
+    assert torch.equal(E, want[0]) and torch.equal(dR1.view(64, 32), want[1]) and torch.equal(dE, want[2])
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=240)
+
+
 def test_a_tuning_loop_over_frames():
     w = W4
     weights = workloads.weights(w)
