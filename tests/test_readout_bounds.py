@@ -1,0 +1,34 @@
+"""CPU: what the bounds of tests/test_gpu_readout_tight.py would notice, with the mistake planted in the float64
+formulas, and that those formulas agree with the oracle's own."""
+import numpy as np
+import pytest
+
+from _readout_bounds import once_rounded, preactivation, stored, unit_energy, weights
+from oracle import tuning
+
+
+def test_stored_is_the_oracles_store():
+    x = np.random.default_rng(0).normal(size=(200, 30)) * np.exp(np.random.default_rng(1).normal(size=(200, 1)))
+    q, e = tuning.store(x)
+    v, scale = stored(x)
+    assert np.array_equal(scale, 2.0 ** np.array(e)) and np.array_equal(v, q * scale[:, None])
+
+
+@pytest.mark.parametrize("F", [18, 64, 98, 128])
+def test_preactivations_are_the_oracles(F):
+    rng = np.random.default_rng(F)
+    x, _ = stored(rng.normal(size=(50, F)))
+    w = weights(F, rng)
+    p, b = preactivation(x, w)
+    assert np.allclose(p, tuning.hidden(x, w), rtol=0, atol=1e-12) and (b > 0).all()
+
+
+@pytest.mark.parametrize("F", [98, 128])
+def test_energies_with_R1_rounded_once_would_be_noticed(F):
+    rng = np.random.default_rng(F)
+    x, _ = stored(rng.normal(size=(1013, F)) * np.exp(0.7 * rng.normal(size=(1013, 1))))
+    w = weights(F, rng)
+    wrong = dict(w, R1=once_rounded(w["R1"]))
+    for h in (0, F // 4 - 1, F // 4, F // 2 - 1):
+        eps, bound = unit_energy(x, w, h)
+        assert (np.abs(tuning.ssp(tuning.hidden(x, wrong)[:, h]) - eps) > 2 * bound).mean() > 0.1
