@@ -1,10 +1,10 @@
 """The readout-tuning kernels against bounds tight enough for what tests/test_readout_bounds.py plants: a hidden layer
-formed from R1 rounded once to 16 bits."""
+formed from R1 rounded once to 16 bits, a tile of atoms left out of the gradients."""
 import numpy as np
 import pytest
 import torch
 
-from _readout_bounds import stored, unit_energy, weights
+from _readout_bounds import GradientProblem, stored, unit_energy, weights
 from schnet_gnn_molecular_b200 import api
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +37,14 @@ def test_energies_hold_both_terms_of_R1(F, n):
         want, bound = unit_energy(x, w, h)
         assert np.all(np.abs(eps.cpu().numpy() - want) <= bound), h
         assert abs(float(E[0]) - want.sum()) <= bound.sum() + 2.0 ** -24 * abs(want.sum())
+
+
+@pytest.mark.parametrize("F", [64, 94, 128])
+def test_gradients_hold_every_tile(F):
+    p = GradientProblem(F)
+    codes, scales = api.store_features(_dev(p.x32))
+    assert np.array_equal(_values(codes, scales, F), p.x)
+    got = api.readout_gradients(codes, scales, _dev(p.off), _dw(p.w), _dev(p.g))
+    for k, want in p.want.items():
+        error = np.abs(got[k].cpu().numpy() - want)
+        assert np.all(error <= p.tol[k]), (k, float((error / p.tol[k]).max()))

@@ -3,7 +3,7 @@ formulas, and that those formulas agree with the oracle's own."""
 import numpy as np
 import pytest
 
-from _readout_bounds import once_rounded, preactivation, stored, unit_energy, weights
+from _readout_bounds import GradientProblem, once_rounded, preactivation, stored, unit_energy, weights
 from oracle import tuning
 
 
@@ -32,3 +32,13 @@ def test_energies_with_R1_rounded_once_would_be_noticed(F):
     for h in (0, F // 4 - 1, F // 4, F // 2 - 1):
         eps, bound = unit_energy(x, w, h)
         assert (np.abs(tuning.ssp(tuning.hidden(x, wrong)[:, h]) - eps) > 2 * bound).mean() > 0.1
+
+
+@pytest.mark.parametrize("F", [64, 94, 128])
+def test_a_tile_left_out_of_the_gradients_would_be_noticed(F):
+    g = GradientProblem(F)
+    R1, sums = g.noticed()
+    assert len(R1) > 15 * 148                     # tiles: rings of 2 and 3 and runs of 8 go round on 148 SMs
+    assert R1.all() and sums.mean() > 0.99       # (where the seed's sign changes inside a tile its halves may cancel)
+    want = tuning.gradients(g.x[:4096], np.minimum(g.off, 4096), g.w, g.g)
+    assert np.allclose(g.tR1[:32].sum(0) * g.r2, want["R1"]) and np.allclose(g.tR2[:32].sum(0), want["R2"])
