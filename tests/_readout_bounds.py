@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import numpy as np
 
+import oracle
 from oracle import tuning
 
 U = 2.0 ** -24
@@ -122,3 +123,20 @@ class GradientProblem:
         R1 = (np.abs(self.tR1 * self.r2) > 2 * self.tol["R1"]).any((1, 2))
         sums = (np.abs(self.tc1 * self.r2) > 2 * self.tol["c1"]).any(1) | (np.abs(self.tR2) > 2 * self.tol["R2"]).any(1)
         return R1, sums
+
+
+def trunk(model: oracle.Model, pos, types, replica_offsets):
+    """The interaction blocks' output x^L in float64: x += ssp(m Wo1 + bo1) Wo2 + bo2 with m the oracle's aggregation."""
+    w = {k: np.asarray(v, dtype=np.float64) for k, v in model.weights.items()}
+    x = w["emb"][types].copy()
+    for l in range(model.L):
+        m = oracle.cfconv(model, l, pos, x @ w["W_in"][l], replica_offsets)
+        x += tuning.ssp(m @ w["Wo1"][l] + w["bo1"][l]) @ w["Wo2"][l] + w["bo2"][l]
+    return x
+
+
+def row_bound(x, scale):
+    """How far stored features may be from the trunk's x: half a step of e4m3 (2^-4 of the value, or 2^-10 of the row's
+    scale) beside 1e-4 of the row's largest for the trunk's own single precision."""
+    d = 1e-4 * np.abs(x).max(1)[:, None]
+    return np.maximum(2.0 ** -4 * (np.abs(x) + d), 2.0 ** -10 * scale[:, None]) + d

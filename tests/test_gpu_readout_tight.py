@@ -1,11 +1,12 @@
 """The readout-tuning kernels against bounds tight enough for what tests/test_readout_bounds.py plants: a hidden layer
-formed from R1 rounded once to 16 bits, a tile of atoms left out of the gradients."""
+formed from R1 rounded once to 16 bits, a tile of atoms left out of the gradients, features in another order."""
 import numpy as np
 import pytest
 import torch
 
-from _readout_bounds import GradientProblem, stored, unit_energy, weights
-from schnet_gnn_molecular_b200 import api
+from _helpers import oracle_model
+from _readout_bounds import GradientProblem, row_bound, stored, trunk, unit_energy, weights
+from schnet_gnn_molecular_b200 import api, workloads
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,29 @@ def test_gradients_hold_every_tile(F):
     for k, want in p.want.items():
         error = np.abs(got[k].cpu().numpy() - want)
         assert np.all(error <= p.tol[k]), (k, float((error / p.tol[k]).max()))
+
+
+@pytest.mark.parametrize("w", [workloads.TINY, workloads.PROTEIN64.with_(name="cg_protein_4x269", n_replicas=4)],
+                         ids=lambda w: w.name)
+@pytest.mark.parametrize("shuffled", [False, True])
+@pytest.mark.parametrize("evaluate", ["energies", "forces", "steps"])
+def test_features_are_the_trunks_in_the_callers_order(w, shuffled, evaluate):
+    W = workloads.weights(w, bias_scale=0.1)
+    off = w.replica_offsets()
+    pos, types = workloads.positions(w).astype(np.float32), workloads.types(w)
+    if shuffled:                                  # beads listed in any order: no list order is the cells'
+        rng = np.random.default_rng(3)
+        order = np.concatenate([a + rng.permutation(b - a) for a, b in zip(off[:-1], off[1:])])
+        pos, types = pos[order], types[order]
+    model = api.from_workload(w, W)
+    p, t = _dev(pos), _dev(types, torch.int32)
+    if evaluate == "steps":
+        model.step(p, torch.zeros_like(p), t, _dev(np.full(w.n_atoms, w.mass, np.float32)), 5, dt=2.0, gamma=0.0,
+                   n_rebuild=2)
+    else:
+        model.build_neighbors(p)
+        model.energy_forces(p, t, forces=evaluate == "forces")
+    codes, scales = model.features()
+    want = trunk(oracle_model(w, W), p.double().cpu().numpy(), types, off)
+    got = _values(codes, scales, w.F)
+    assert np.all(np.abs(got - want) <= row_bound(want, scales.double().cpu().numpy()))

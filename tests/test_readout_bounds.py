@@ -3,8 +3,11 @@ formulas, and that those formulas agree with the oracle's own."""
 import numpy as np
 import pytest
 
-from _readout_bounds import GradientProblem, once_rounded, preactivation, stored, unit_energy, weights
+import oracle
+from _helpers import oracle_model
+from _readout_bounds import GradientProblem, once_rounded, preactivation, row_bound, stored, trunk, unit_energy, weights
 from oracle import tuning
+from schnet_gnn_molecular_b200 import workloads
 
 
 def test_stored_is_the_oracles_store():
@@ -42,3 +45,22 @@ def test_a_tile_left_out_of_the_gradients_would_be_noticed(F):
     assert R1.all() and sums.mean() > 0.99       # (where the seed's sign changes inside a tile its halves may cancel)
     want = tuning.gradients(g.x[:4096], np.minimum(g.off, 4096), g.w, g.g)
     assert np.allclose(g.tR1[:32].sum(0) * g.r2, want["R1"]) and np.allclose(g.tR2[:32].sum(0), want["R2"])
+
+
+@pytest.mark.parametrize("w", [workloads.TINY, workloads.PROTEIN64.with_(name="cg_protein_4x269", n_replicas=4)],
+                         ids=lambda w: w.name)
+def test_features_of_another_atom_would_be_noticed(w):
+    """The trunk's formula is the oracle's (its energies follow from it), and no atom's features pass for another's."""
+    W = workloads.weights(w, bias_scale=0.1)
+    model = oracle_model(w, W)
+    pos, types, off = workloads.positions(w).astype(np.float64), workloads.types(w), w.replica_offsets()
+    x = trunk(model, pos, types, off)
+    _, eps, _ = oracle.energy_forces(model, pos, types, off, forces=False)
+    mine = tuning.ssp(tuning.hidden(x, W)) @ W["R2"].astype(np.float64) + W["c2"]
+    assert np.allclose(mine, eps, rtol=0, atol=1e-10)
+    v, scale = stored(x)
+    bound = row_bound(x, scale)
+    assert (np.abs(v - x) <= bound).all()
+    for i in range(len(x)):
+        same = (np.abs(v - x[i]) <= row_bound(x[i:i + 1], scale[i:i + 1])).all(1)
+        assert same.sum() == 1 and same[i]
