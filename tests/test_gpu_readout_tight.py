@@ -51,7 +51,37 @@ def test_gradients_hold_every_tile(F):
         assert np.all(error <= p.tol[k]), (k, float((error / p.tol[k]).max()))
 
 
-@pytest.mark.parametrize("w", [workloads.TINY, workloads.PROTEIN64.with_(name="cg_protein_4x269", n_replicas=4)],
+def test_rows_past_32_bits():
+    """17 million rows of 128: the codes' bytes and the features' elements pass 2^31.  The last rows' results are those
+    of the last rows alone."""
+    n, tail, F = 17_000_000, 1280, 128
+    rng = np.random.default_rng(4)
+    x = torch.zeros(n, F, device="cuda")
+    last = rng.normal(size=(tail, F)).astype(np.float32)
+    x[-tail:] = _dev(last)
+    codes, scales = api.store_features(x)
+    del x
+    want = api.store_features(_dev(last))
+    assert all(torch.equal(a[-tail:].view(torch.uint8), b.view(torch.uint8)) for a, b in zip((codes, scales), want))
+    assert not codes[:-tail].view(torch.uint8).any()
+    w = _dw(weights(F, rng))
+    E, eps = api.readout_energy(codes, scales, _dev([0, n - 700, n], torch.int32), w)
+    E1, eps1 = api.readout_energy(*want, _dev([0, tail - 700, tail], torch.int32), w)
+    assert n % 128 == 64 and tail % 128 == 0       # (the same rows at other places of a tile)
+    assert torch.equal(eps[-tail:], eps1)
+    assert abs(float(E[1] - E1[1])) <= 2.0 ** -24 * abs(float(E1[1]))
+    g = _dev([0.0, 1.0], torch.float32)
+    got = api.readout_gradients(codes, scales, _dev([0, n - 700, n], torch.int32), w, g)
+    alone = api.readout_gradients(*want, _dev([0, tail - 700, tail], torch.int32), w, g)
+    assert float(got["c2"]) == 700.0
+    for k in got:                                  # the same terms, summed in other tiles: 700 roundings of them
+        size = {"R1": np.abs(last[-700:]).sum(0)[:, None] * w["R2"].abs().cpu().numpy(),
+                "c1": 700 * w["R2"].abs().cpu().numpy(), "R2": np.full(F // 2, 700 * 4.0), "c2": 0.0}[k]
+        assert np.all(np.abs((got[k] - alone[k]).cpu().numpy()) <= 700 * 2.0 ** -23 * size), k
+
+
+@pytest.mark.parametrize("w", [workloads.TINY, workloads.TINY.with_(name="tiny_chain64_f50", F=50),
+                               workloads.PROTEIN64.with_(name="cg_protein_4x269", n_replicas=4)],
                          ids=lambda w: w.name)
 @pytest.mark.parametrize("shuffled", [False, True])
 @pytest.mark.parametrize("evaluate", ["energies", "forces", "steps"])
