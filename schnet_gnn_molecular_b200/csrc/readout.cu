@@ -290,6 +290,24 @@ struct StageR1 {
     }
 };
 
+// log2((1 + 2^t) / 2) for |t| <= 3 as t / 2 and an even polynomial (ssp2_fit.py; relative error 2e-7),
+// for a warp's units whose t are all this small; which they are is looked at 8 at a time.
+// The MUFU logarithm errs by up to 2^-22 around 1 and by 6e-8 on average, the same way for every
+// atom: with it alone the energies of 64 chains are off by 2-7e-6, 2-5e-5 and 1-7e-4 of themselves
+// at a tenth, hundredth and thousandth of Xavier weights, dR2 by 6e-6, 4e-5 and 8e-4; with this
+// both by 1-3e-7 (torch's float32 forms: energies 4-9e-7, 3e-6, 3-9e-5, dR2 6e-7, 3e-6, 7e-5).
+constexpr float SSP2_SMALL = 3.f;
+__device__ __forceinline__ float2 ssp2_small(float2 t)
+{
+    const float2 s = mul2(t, t);
+    float2 q = fma2(dup2(-1.0950124140762796e-09f), s, dup2(6.010890274410485e-08f));
+    q = fma2(q, s, dup2(-1.9344583961355966e-06f));
+    q = fma2(q, s, dup2(5.532750947168097e-05f));
+    q = fma2(q, s, dup2(-0.0017342476639896631f));
+    q = fma2(q, s, dup2(0.08664331585168839f));
+    return mul2(t, fma2(t, q, dup2(0.5f)));
+}
+
 // the factor that takes an accumulator of row i (codes times R1 2^s) to p log2(e)
 __device__ __forceinline__ float row_factor(int byte, float down)
 {
@@ -332,11 +350,14 @@ __device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l
 // One thread per atom with four groups of 4 warps (96 registers): 195 us.  Widening warps
 // apart, D doubled (64 registers): 176 us for 171, and 1 us more for small calls.
 // 269 atoms: 8.0 us with the sums' kernel.
+// The look whether 8 units are all small (ssp2_small) costs 5 % at 4.2 M atoms, so a warp takes it at
+// every 8th tile and as long as it finds any: 218 us for 217 without it.
 // FW is the width that codes and hidden layer are padded to: 64 up to 64 features (a thread
 // has 32 codes and 16 units, the MMAs half their K and N), else 128.  At 64 features the
 // 64 form takes 115 us for 4.2 M atoms against 184 of the 128 form, and 16.4 against 19 for
 // 192,000; the same choice made at run time inside one kernel cost 128 features 14 %.
 constexpr int FWD_GROUPS = 3, FWD_STAGES = 3, FWD_GT = 256, FWD_THREADS = FWD_GROUPS * FWD_GT + 32;
+constexpr int FWD_LOOK = 8;                                      // tiles from look to look
 constexpr uint32_t FWD_R1 = FWD_GROUPS * FWD_STAGES * TILE_BYTES;
 constexpr uint32_t FWD_CST = FWD_R1 + 2 * R1_TERM;               // float4[32]: c1 log2e, R2 ln2 of two units
 constexpr uint32_t FWD_RED = FWD_CST + 32 * 16;
@@ -466,6 +487,7 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             __syncwarp();
             if (ok && (t & 31) == 0) mbar_arrive(full + FWD_STAGES);
         };
+        bool found = false;                                       // whether the warp's last look found small units
         int byte = scale_of(0);
         if (nt > 0) {
             widen(0);
@@ -483,14 +505,51 @@ k_readout_eps(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
             tmem_ld_wait();
             if (it + 1 < nt) hand_over();
             float2 e0 = make_float2(c2, 0.f), e1 = make_float2(0.f, 0.f);
+            if (found || it % FWD_LOOK == 0) {
+                found = false;
 #pragma unroll
-            for (int j = 0; j < HT / 2; ++j) {
-                const float4 c = cst[half * (HT / 2) + j];
-                const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
-                const float2 u = make_float2(ex2_mufu(-fabsf(p.x)), ex2_mufu(-fabsf(p.y)));
-                const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
-                e0 = fma2(make_float2(c.z, c.w), make_float2(lg2_mufu(y.x), lg2_mufu(y.y)), e0);
-                e1 = fma2(make_float2(c.z, c.w), make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)), e1);
+                for (int j0 = 0; j0 < HT / 2; j0 += 4) {              // 8 units at a time
+                    float2 p[4], y[4];
+                    float most = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = j0 + k;
+                        const float4 c = cst[half * (HT / 2) + j];
+                        p[k] = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
+                        most = fmaxf(fmaxf(most, fabsf(p[k].x)), fabsf(p[k].y));
+                    }
+                    const bool small = __all_sync(0xffffffffu, most <= SSP2_SMALL);
+                    found |= small && half * HT + 2 * j0 < a.H;       // (units that the layer does not have are 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = fma2(dup2(0.5f), make_float2(ex2_mufu(-fabsf(p[k].x)), ex2_mufu(-fabsf(p[k].y))),
+                                    dup2(0.5f));
+                    auto sums = [&](auto poly) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 c = cst[half * (HT / 2) + j0 + k];
+                            const float2 r2 = make_float2(c.z, c.w);
+                            if (poly) {
+                                e0 = fma2(r2, ssp2_small(p[k]), e0);
+                            } else {
+                                e0 = fma2(r2, make_float2(lg2_mufu(y[k].x), lg2_mufu(y[k].y)), e0);
+                                e1 = fma2(r2, make_float2(max_nan(p[k].x, 0.f), max_nan(p[k].y, 0.f)), e1);
+                            }
+                        }
+                    };
+                    if (small) sums(std::true_type{});
+                    else sums(std::false_type{});
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < HT / 2; ++j) {
+                    const float4 c = cst[half * (HT / 2) + j];
+                    const float2 p = fma2(make_float2(d[2 * j], d[2 * j + 1]), kk, make_float2(c.x, c.y));
+                    const float2 u = make_float2(ex2_mufu(-fabsf(p.x)), ex2_mufu(-fabsf(p.y)));
+                    const float2 y = fma2(dup2(0.5f), u, dup2(0.5f));
+                    e0 = fma2(make_float2(c.z, c.w), make_float2(lg2_mufu(y.x), lg2_mufu(y.y)), e0);
+                    e1 = fma2(make_float2(c.z, c.w), make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f)), e1);
+                }
             }
             const int i = first_row(g, it) + t;
             float e = (e0.x + e0.y) + (e1.x + e1.y);
@@ -626,22 +685,6 @@ __device__ __forceinline__ float rcp_mufu(float x)
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// log2((1 + 2^t) / 2) for |t| <= 3 as t / 2 and an even polynomial (ssp2_fit.py; relative error 2e-7).
-// The MUFU logarithm errs by up to 2^-22 around 1 and by 6e-8 on average: with it alone dR2 of 64
-// chains is off by 6e-6, 4e-5 and 8e-4 of itself at a tenth, hundredth and thousandth of Xavier
-// weights, with this 3e-7, 1.2e-7 and 1.2e-7 (torch's float32 forms: 6e-7, 3e-6 and 7e-5).
-constexpr float SSP2_SMALL = 3.f;
-__device__ __forceinline__ float2 ssp2_small(float2 t)
-{
-    const float2 s = mul2(t, t);
-    float2 q = fma2(dup2(-1.0950124140762796e-09f), s, dup2(6.010890274410485e-08f));
-    q = fma2(q, s, dup2(-1.9344583961355966e-06f));
-    q = fma2(q, s, dup2(5.532750947168097e-05f));
-    q = fma2(q, s, dup2(-0.0017342476639896631f));
-    q = fma2(q, s, dup2(0.08664331585168839f));
-    return mul2(t, fma2(t, q, dup2(0.5f)));
 }
 
 // Seeds: gat[i] = g of atom i's replica (0 outside all replicas), and a CTA's share of
@@ -972,7 +1015,8 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int c = q * 8 + 2 * j;
-                        const float2 sp2 = poly ? ssp2_small(t[j]) : add2(t[j], make_float2(lg2_mufu(y[j].x), lg2_mufu(y[j].y)));
+                        const float2 sp2 = poly ? ssp2_small(t[j])
+                                                : add2(t[j], make_float2(lg2_mufu(y[j].x), lg2_mufu(y[j].y)));
                         const float2 a2 = fma2(dup2(gi), sp2, make_float2(acc2[c], acc2[c + 1]));
                         acc2[c] = a2.x; acc2[c + 1] = a2.y;
                     }

@@ -1,5 +1,5 @@
 """Coefficients of the shifted softplus of small arguments, used by ``ssp2_small`` in
-``csrc/readout.cu`` (the readout's gradients, where the MUFU logarithm's absolute error,
+``csrc/readout.cu`` (readout energies and gradients, where the MUFU logarithm's absolute error,
 2^-22 around 1, would be most of a small activation).
 
 In base 2, ssp2(t) = log2((1 + 2^t) / 2) = t / 2 + log2(cosh(t ln2 / 2)): an odd linear part, which

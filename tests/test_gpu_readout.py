@@ -281,6 +281,27 @@ def test_hidden_layers_of_zero_add_nothing_to_dR2(F, zero):
     assert not got["R2"].any()
 
 
+@pytest.mark.parametrize("n", [1000, 500_009])                  # up to 9 tiles a group: looked at twice
+@pytest.mark.parametrize("F", [18, 64, 128])
+def test_energies_of_small_activations(F, n):
+    """p = c1 from 1e-6 to 2 in size, one hidden unit at a time: eps to 2e-7 (the activation) and 4u (c1 log2 e and its
+    product, R2 ln2 and its), E to u more."""
+    rng = np.random.default_rng(F)
+    H = F // 2
+    codes, scales, _ = _stored(n, F, rng)
+    w = _weights(F, rng)
+    w["R1"][:] = 0
+    w["c1"] = (np.geomspace(1e-6, 2.0, H) * np.where(np.arange(H) % 2, 1, -1)).astype(np.float32)
+    w["c2"][:] = 0
+    p = w["c1"].astype(np.float64)
+    want = np.log1p(np.expm1(p) / 2.0)                                   # ssp(p) without cancellation
+    for h in range(H) if n == 1000 else (0, H // 2, H - 1):
+        w["R2"] = np.eye(H, dtype=np.float32)[h]
+        E, eps = api.readout_energy(codes, scales, _dev([0, n], torch.int32), _dw(w))
+        assert np.all(np.abs(eps.cpu().numpy() - want[h]) <= (2e-7 + 4 * U) * abs(want[h])), h
+        assert abs(float(E[0]) - n * want[h]) <= (2e-7 + 5 * U) * n * abs(want[h]), h
+
+
 @pytest.mark.parametrize("F", [18, 64, 128])
 def test_dR2_of_small_activations(F):
     """p = c1 from 1e-6 to 2 in size: each term of dR2 to 2e-7 (the activation) and 3u (c1 log2 e and its product),
