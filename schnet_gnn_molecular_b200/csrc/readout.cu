@@ -5,7 +5,7 @@
 // Store: per row (at most 128 features, one block) the scale is a power of two, so
 // x / scale is exact and the e4m3 rounding is the only one: codes are a function of
 // x alone, whatever computes them.  It is bound by HBM: 641 bytes a float32 row of 128,
-// 10^6 rows in 107 us (92 % of a copy's rate).
+// 10^6 rows in 107 us on the device (92 % of a copy's rate), 117 a call back to back.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -345,16 +345,18 @@ __device__ __forceinline__ double replica_sum(const ReadoutArgs& a, int r, int l
 // warp and only then works on D(it), which hides the MMAs.  The issuing thread blocks while
 // the tensor core's queue is full, so it does nothing else.
 // Bound: 2 transcendentals per hidden unit on the MUFU, 8 cycles an atom and SM (HBM: 133
-// bytes, 5.9 cycles; MMAs: 4).  Exponentials on the FMA pipe (one pair in 8, 4, 2) cost more
-// issue slots than they free on the MUFU: 180, 186, 192 us against 180 for 4.2 M atoms.
-// One thread per atom with four groups of 4 warps (96 registers): 195 us.  Widening warps
-// apart, D doubled (64 registers): 176 us for 171, and 1 us more for small calls.
+// bytes, 5.9 cycles; MMAs: 4).  4.2 M atoms: 187 us in short runs, 222 for seconds on end (the
+// power cap).  Tried, in short runs against 180 before the small units had their polynomial:
+// exponentials on the FMA pipe (one pair in 8, 4, 2) cost more issue slots than they free on the
+// MUFU, 180, 186, 192 us; one thread per atom with four groups of 4 warps (96 registers) 195;
+// widening warps apart, D doubled (64 registers) 176 us for 171, and 1 us more for small calls.
 // 269 atoms: 8.0 us with the sums' kernel.
 // The look whether 8 units are all small (ssp2_small) costs 5 % at 4.2 M atoms, so a warp takes it at
-// every 8th tile and as long as it finds any: 218 us for 217 without it.
+// every 8th tile and as long as it finds any: 218 us for 217 without it.  So an atom's eps may
+// differ by that polynomial's rounding with the atoms that share its warp, not from call to call.
 // FW is the width that codes and hidden layer are padded to: 64 up to 64 features (a thread
 // has 32 codes and 16 units, the MMAs half their K and N), else 128.  At 64 features the
-// 64 form takes 115 us for 4.2 M atoms against 184 of the 128 form, and 16.4 against 19 for
+// 64 form takes 117 us for 4.2 M atoms against 187 of the 128 form, and 15.9 against 20.5 for
 // 192,000; the same choice made at run time inside one kernel cost 128 features 14 %.
 constexpr int FWD_GROUPS = 3, FWD_STAGES = 3, FWD_GT = 256, FWD_THREADS = FWD_GROUPS * FWD_GT + 32;
 constexpr int FWD_LOOK = 8;                                      // tiles from look to look
@@ -639,10 +641,11 @@ static schnet_status launch_sums(const ReadoutArgs& a, cudaStream_t s)
 // shared memory: 10, HBM: 5.8).  It takes 24: its 20 warps issue every second cycle, each
 // waiting ~10 cycles an instruction (without its transcendentals 353 us for 373 at 4.2 M
 // atoms, before D2 was doubled), and registers and shared memory hold no more of them.
-// 4.2 M atoms: 335-355 us, 383 under the power cap; 545 with every warp widening its own rows.
+// 4.2 M atoms: 342 us in short runs, 393 under the power cap; 545 with every warp widening its own
+// rows.
 // FW as in the energies: in the 64 form a thread has 8 units, GEMM2's N is 64, and what the
-// unused half of X's features puts into D2 is not read.  At 64 features it takes 240 us for
-// 4.2 M atoms against 333 of the 128 form, and 26 against 33.5 for 192,000.
+// unused half of X's features puts into D2 is not read.  At 64 features it takes 239 us for
+// 4.2 M atoms against 342 of the 128 form, and 25 against 34 for 192,000.
 constexpr int GRAD_EPI = 512, GRAD_THREADS = GRAD_EPI + 128, GRAD_XS = 3;
 constexpr int GRAD_FLUSH = 8, GRAD_FOLD = 32;
 constexpr uint32_t GRAD_OP = 128 * 128 * 2;                      // codes as fp16 [128][128], or [128][64 hi | 64 residual]
