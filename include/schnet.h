@@ -370,7 +370,8 @@ SCHNET_API schnet_status schnet_set_readout(schnet_ctx *ctx, const float *h_R1, 
  *   d_workspace: device, schnet_readout_workspace_bytes, 256-byte aligned
  * 0 <= n_atoms <= 0x7fff0000, 1 <= n_replicas <= 0x7ff00000.  A NaN or an infinity in R1 or c1 makes all
  * results NaN; hidden pre-activations, and a row's scale times the largest |R1|, are to stay below 2^126
- * in magnitude.  A device-side wait that gives up makes all results NaN.  Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
+ * in magnitude.  A device-side wait that gives up makes all results NaN.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_features as above), CUDA. */
 SCHNET_API schnet_status schnet_readout_energy(const uint8_t *d_codes, const uint8_t *d_scales, int32_t n_atoms,
                                                int32_t n_features, int32_t n_replicas,
                                                const int32_t *d_replica_offsets, const float *d_R1,

@@ -24,7 +24,8 @@ EXPORTED = ["schnet_workspace_bytes", "schnet_create", "schnet_build_neighbors",
             "schnet_get_neighbors", "schnet_get_atom_energies", "schnet_kernel_launches", "schnet_profile_steps",
             "schnet_build_neighbors_noalloc", "schnet_test_exp2", "schnet_test_timeout", "schnet_store_features",
             "schnet_get_features", "schnet_set_readout", "schnet_readout_energy", "schnet_readout_gradients",
-            "schnet_readout_workspace_bytes", "schnet_test_readout_timeout", "schnet_preference_loss", "schnet_preference_workspace_bytes"]
+            "schnet_readout_workspace_bytes", "schnet_test_readout_timeout", "schnet_preference_loss",
+            "schnet_preference_workspace_bytes"]
 KERNEL_CLASSES = ["cfconv_fwd", "cfconv_bwd", "atomwise", "neighbors", "forces", "integrate", "reduce", "mask",
                   "cfconv_dh"]
 

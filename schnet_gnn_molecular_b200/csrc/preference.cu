@@ -265,7 +265,8 @@ using namespace schnet;
 
 extern "C" schnet_status schnet_preference_workspace_bytes(int32_t n_replicas, int64_t n_pairs, size_t* bytes)
 {
-    if (!bytes || n_replicas < 1 || n_replicas > MAX_REPLICAS || n_pairs < 0 || n_pairs > 0x7fffffffLL) return SCHNET_ERR_INVALID_ARG;
+    if (!bytes || n_replicas < 1 || n_replicas > MAX_REPLICAS || n_pairs < 0 || n_pairs > 0x7fffffffLL)
+        return SCHNET_ERR_INVALID_ARG;
     PrefArgs a{};
     *bytes = pref_carve(n_replicas, nullptr, a);
     return SCHNET_OK;
@@ -279,8 +280,8 @@ extern "C" schnet_status schnet_preference_loss(const void* d_energy, const void
 {
     size_t need = 0;
     if (!d_energy || !d_loss || !d_grad_energy || !d_workspace || ((uintptr_t)d_workspace & 255) ||
-        (dtype != SCHNET_FLOAT32 && dtype != SCHNET_FLOAT64) || !(kT > 0.0) || !std::isfinite(kT) || !std::isfinite(1.0 / kT) ||
-        !(smoothing >= 0.0 && smoothing <= 1.0) ||
+        (dtype != SCHNET_FLOAT32 && dtype != SCHNET_FLOAT64) || !(kT > 0.0) || !std::isfinite(kT) ||
+        !std::isfinite(1.0 / kT) || !(smoothing >= 0.0 && smoothing <= 1.0) ||
         schnet_preference_workspace_bytes(n_replicas, n_pairs, &need) != SCHNET_OK || ws_bytes < need ||
         (n_pairs > 0 && !d_pairs) || ((uintptr_t)d_pairs & 7))
         return SCHNET_ERR_INVALID_ARG;

@@ -973,7 +973,8 @@ k_readout_grad(const __grid_constant__ CUtensorMap map, ReadoutArgs a)
                 const int byte = bytes[x * 128 + row];
                 k = row_factor(byte, down);
                 if (k != k) gi = k;
-                gx = gi * __uint_as_float((uint32_t)byte << 23) * __uint_as_float((uint32_t)(126 + E) << 23);   // half: of 2 sigma
+                // (half of it: the factor is 2 sigma)
+                gx = gi * __uint_as_float((uint32_t)byte << 23) * __uint_as_float((uint32_t)(126 + E) << 23);
             }
             x = next(x);
             if (it >= 2 && !wait(done2, it - 2)) break;           // B is free
@@ -1151,8 +1152,8 @@ static schnet_status readout_args(const uint8_t* codes, const uint8_t* scales, i
 {
     if (F < 2 || F > FP || (F & 1)) return SCHNET_ERR_UNSUPPORTED;
     size_t need = 0;
-    if (n < 0 || n > MAX_ATOMS || R < 1 || R > MAX_REPLICAS || !off || !R1 || !c1 || !R2 || !c2 || !ws || ((uintptr_t)ws & 255) ||
-        (n > 0 && (!codes || !scales || ((uintptr_t)codes & 15))) ||
+    if (n < 0 || n > MAX_ATOMS || R < 1 || R > MAX_REPLICAS || !off || !R1 || !c1 || !R2 || !c2 || !ws ||
+        ((uintptr_t)ws & 255) || (n > 0 && (!codes || !scales || ((uintptr_t)codes & 15))) ||
         schnet_readout_workspace_bytes(n, F, &need) != SCHNET_OK || ws_bytes < need)
         return SCHNET_ERR_INVALID_ARG;
     a.codes = codes; a.scales = scales; a.n = n; a.F = F; a.H = F / 2; a.W = (F + 15) / 16 * 16; a.R = R;
