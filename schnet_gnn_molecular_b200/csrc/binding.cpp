@@ -190,6 +190,9 @@ PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n_args)
     if (!arity(n_args, 6)) return nullptr;
     const Tensor &energy = tensor(args[0], "energy"), &pairs = tensor(args[1], "pairs");
     const Tensor* ref = args[2] == Py_None ? nullptr : &tensor(args[2], "reference");
+    const Tensor* bits = args[3] == Py_None ? nullptr : &tensor(args[3], "flags");
+    if (bits && bits->scalar_type() != ScalarType::Int && bits->scalar_type() != ScalarType::UInt32)
+        refuse("flags must be one 32-bit integer on the energies' device");
     const ScalarType t = energy.scalar_type();
     if (!energy.is_cuda() || energy.dim() != 1 || energy.size(0) < 1 || !energy.is_contiguous() ||
         (t != ScalarType::Float && t != ScalarType::Double))
@@ -205,11 +208,10 @@ PyObject* preference_loss(PyObject*, PyObject* const* args, Py_ssize_t n_args)
         reference = ref->data_ptr();
     }
     uint32_t* flags = nullptr;
-    if (args[3] != Py_None) {
-        const Tensor& f = tensor(args[3], "flags");
-        if (!f.is_cuda() || f.get_device() != dev || f.numel() != 1 || f.element_size() != 4)
+    if (bits) {
+        if (!bits->is_cuda() || bits->get_device() != dev || bits->numel() != 1)
             refuse("flags must be one 32-bit integer on the energies' device");
-        flags = ptr<uint32_t>(f);
+        flags = ptr<uint32_t>(*bits);
     }
     const double kT = PyFloat_AsDouble(args[4]), smoothing = PyFloat_AsDouble(args[5]);
     if (PyErr_Occurred()) return nullptr;

@@ -152,3 +152,13 @@ def test_binding_refuses_what_autograd_would_lose(lib):
                 call(value)
             with pytest.raises(ValueError, match="CUDA"):
                 call(value.detach())
+
+
+def test_binding_refuses_flags_that_are_no_integer(lib):
+    E, pairs = torch.zeros(4), torch.zeros(1, 2, dtype=torch.int32)
+    for t in (torch.float32, torch.int64, torch.int16):
+        with pytest.raises(ValueError, match="flags must be one 32-bit integer"):
+            api.preference_loss(E, pairs, kT=1.0, flags=torch.zeros(1, dtype=t))
+    for t in (torch.int32, torch.uint32):
+        with pytest.raises(ValueError, match="CUDA"):
+            api.preference_loss(E, pairs, kT=1.0, flags=torch.zeros(1, dtype=t))
